@@ -38,7 +38,26 @@
  * that pa_device_errors() returns and clears.  pa_last_error() gives a
  * message for the last failing call on the calling thread.
  *
- * Supported: block_size 16; head_dim 64 or 128; dtype fp32, fp16, bf16.
+ * 4-bit pools (dtype PA_Q4_F16 / PA_Q4_BF16) hold K and V at 4.5 bits a value;
+ *                    q, out, k_new and v_new stay fp16 / bf16.  k_pool and
+ *                    v_pool are [num_blocks][heads][9 * head_dim] bytes.  The
+ *                    tile of one (block, head) is
+ *                      [0, 8 D)   [D / 32 pieces][16 tokens][16 bytes], byte b
+ *                                 of piece c holding dimension 32 c + 2 b in its
+ *                                 low half and 32 c + 2 b + 1 in its high half;
+ *                      [8 D, 9 D) [D / 64 groups][16 tokens] 32-bit words: the
+ *                                 scale s (bf16) in the upper half, the zero
+ *                                 point z (a whole number, fp16) in the lower.
+ *                    A held number n stands for s * (n - z).  Of 64 values x of
+ *                    one token and head, s = bf16(max((max x - min x) / 15,
+ *                    max |x| / 2000)), z = round(-min x / s) and n =
+ *                    clamp(round(x / s) + z, 0, 15), halves to even (n = z = 0
+ *                    where s = 0).  A group that holds an infinity or NaN, or
+ *                    whose range passes fp32, reads back as NaN.
+ *
+ * Supported: block_size 16; head_dim 64 or 128; dtype fp32, fp16, bf16, and
+ * 4 bits with fp16 or bf16.  Prefill and shared-prefix decode take fp16 and
+ * bf16 pools (pa_convert_blocks reads 4-bit blocks back for them).
  */
 #ifndef PAGEDATTN_H
 #define PAGEDATTN_H
@@ -50,7 +69,13 @@
 extern "C" {
 #endif
 
-typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2 } pa_dtype;
+typedef enum {
+  PA_F32 = 0,
+  PA_F16 = 1,
+  PA_BF16 = 2,
+  PA_Q4_F16 = 3, /* 4-bit pools; q, out, k_new, v_new fp16 */
+  PA_Q4_BF16 = 4 /* 4-bit pools; q, out, k_new, v_new bf16 */
+} pa_dtype;
 
 typedef enum {
   PA_OK = 0,
@@ -80,11 +105,13 @@ typedef struct pa_pool {
   int32_t heads;
   int32_t head_dim;
   int32_t dtype;       /* pa_dtype */
-  int32_t elem_bytes;
+  int32_t elem_bytes;   /* of q, out, k_new, v_new, and of a 16- or 32-bit pool */
   int32_t q_per_kv;     /* query heads per KV head: 1 (MHA), 2, 4 or 8 (GQA/MQA) */
-  int64_t token_stride; /* elements between consecutive slots of a block: head_dim */
-  int64_t head_stride;  /* elements between heads of a block: block_size * head_dim */
-  int64_t block_stride; /* elements between blocks: heads * block_size * head_dim */
+  int64_t token_stride; /* elements between consecutive slots of a block: head_dim
+                           (4-bit: bytes between the pieces of two tokens, 16) */
+  int64_t head_stride;  /* elements between heads of a block: block_size * head_dim
+                           (4-bit: bytes, 9 * head_dim) */
+  int64_t block_stride; /* elements between blocks: heads * head_stride (4-bit: bytes) */
   int64_t bytes_per_pool; /* bytes of ONE of k_pool / v_pool */
 } pa_pool;
 
@@ -112,7 +139,7 @@ pa_status pa_pool_set_query_heads(pa_pool* pool, int32_t num_q_heads);
  * Write each new token's K and V rows into the slot slot_mapping names:
  * k_pool[slot / bs][h][slot % bs][:] = k_new[t][h][:] for every head, the
  * same for V (7minutos.es section 2: the new token goes into the tail page).
- * Bit copy.  A negative slot is skipped; a slot >= num_blocks * block_size
+ * Bit copy (4-bit pools: quantised).  A negative slot is skipped; a slot >= num_blocks * block_size
  * sets PA_DEVERR_SLOT and is skipped.  num_tokens == 0 is a no-op.
  */
 pa_status pa_reshape_and_cache(const pa_pool* pool, const void* k_new, const void* v_new,
@@ -206,7 +233,8 @@ pa_status pa_decode_attention_planned(const pa_pool* pool, const void* q, const 
  * sequence s is written at its position context_lens[s] - 1, i.e. slot
  * block_tables[s][(L-1)/bs] * bs + (L-1) % bs, and attended to with the rest.
  * The pools after the call, and the output, are bit-identical to the two
- * separate calls.  Sequences of length 0 append nothing.  The block holding
+ * separate calls (4-bit pools: the new token is quantised by a launch of its
+ * own before the attention).  Sequences of length 0 append nothing.  The block holding
  * the new token must be private to its sequence (copy it on write first, as
  * for pa_reshape_and_cache).  The planned form takes a plan written by
  * pa_decode_plan, with the same rules as pa_decode_attention_planned.
@@ -346,6 +374,105 @@ pa_status pa_device_errors(void* stream, uint32_t* flags);
  * failure path without a GPU fault.
  */
 pa_status pa_selftest_wait_timeout(void* stream);
+
+/*
+ * Whole blocks from one pool into another of a different width: for every
+ * pair (src_block of the first pool, dst_block of the second), every head, K
+ * and V.  One pool is fp16 (bf16) and the other PA_Q4_F16 (PA_Q4_BF16), with
+ * the same heads and head_dim.  A prompt's blocks go from the prefill's pool
+ * to 4 bits this way, and back for a later chunk's prefill; read back, a
+ * value is rounded once to the 16-bit type and held within its finite range.
+ * pairs is read on the device; a pair outside either pool sets PA_DEVERR_PAIR
+ * and is skipped.  Two pairs of one call must not name the same dst_block.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (any other pair of types),
+ *         PA_ERR_CUDA.
+ */
+pa_status pa_convert_blocks(const pa_pool* src, const void* k_src, const void* v_src,
+                            const pa_pool* dst, void* k_dst, void* v_dst, const int32_t* pairs,
+                            int32_t num_pairs, void* stream);
+
+/*
+ * Decode attention that also gathers every cached token's attention weight,
+ * the measure that pa_evict_tokens evicts by:
+ *   out as pa_decode_attention (the same bits), and for t < context_lens[s]
+ *   mass_out[s][t] = decay * mass_in[s][t] + sum over query heads h of
+ *                    softmax_t(scale * q[s][h] . K_t).
+ * mass_in, mass_out: fp32 [num_seqs][mass_stride], mass_stride at least the
+ * longest context (max_context_len); they may be the same buffer, else they
+ * must not overlap; mass_in NULL counts as zero.  Entries at or past a
+ * sequence's length are neither read nor written.  The heads are added in
+ * order in fp32, so the result does not change from run to run.  All pool
+ * types.  At most 65535 sequences.
+ * workspace: pa_decode_mass_workspace_bytes() (the decode workspace, then 4
+ * bytes per query head and token of every sequence's longest context).  The planned form
+ * takes a plan that pa_decode_plan wrote into the same workspace, with the
+ * rules of pa_decode_attention_planned.
+ */
+pa_status pa_decode_mass_workspace_bytes(const pa_pool* pool, int32_t num_seqs,
+                                         int32_t max_blocks_per_seq, int32_t max_context_len,
+                                         int32_t partition_size, size_t* bytes);
+
+pa_status pa_decode_attention_mass(const pa_pool* pool, const void* q, const void* k_pool,
+                                   const void* v_pool, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                   int32_t num_seqs, int32_t max_context_len, float scale, void* out,
+                                   const float* mass_in, float* mass_out, int64_t mass_stride,
+                                   float decay, void* workspace, size_t workspace_bytes,
+                                   int32_t partition_size, void* stream);
+
+pa_status pa_decode_attention_mass_planned(const pa_pool* pool, const void* q, const void* k_pool,
+                                           const void* v_pool, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, int32_t num_seqs,
+                                           int32_t max_context_len, float scale, void* out,
+                                           const float* mass_in, float* mass_out,
+                                           int64_t mass_stride, float decay, void* workspace,
+                                           size_t workspace_bytes, int32_t partition_size,
+                                           void* stream);
+
+/* What eviction knows of every sequence's cached tokens, in slots of the
+ * sequence (0 .. context_len - 1).  All zero is the state of a new sequence
+ * whose slot t holds position t. */
+typedef struct pa_track {
+  float* mass;        /* [num_seqs][stride] gathered weight of the token in slot t */
+  int32_t* positions; /* [num_seqs][stride] original position of the token in slot t < held */
+  int32_t* history;   /* [num_seqs][2] = (held, next): slots from `held` on arrived since the
+                         last eviction, in order, from position `next` on */
+  int64_t stride;     /* tokens between sequences, at least the longest context */
+} pa_track;
+
+/*
+ * Evict tokens of every sequence that is over its budget, in place: of
+ * context_lens[s] cached tokens keep_lens[s] stay, in slots 0 ..
+ * keep_lens[s] - 1, and the sequence's length is keep_lens[s] from then on
+ * (the caller's context_lens and block manager; blocks past it can be
+ * released).  Sequences at or below their budget stay as they are.
+ * Who stays: first the protected tokens, those whose original position is
+ * below `sinks` or among the last `recent` seen; then those of largest mass.
+ * Ties, and protected tokens beyond the budget, go by the lowest slot.  NaN
+ * counts above every number.
+ * Where: attention does not depend on the order of cached tokens.  A token
+ * that stays and is in a slot below keep_lens[s] is not moved; the i-th one in
+ * a slot from keep_lens[s] on moves to the i-th slot below that falls free.
+ * `out` receives the track after it (mass 0 from keep_lens[s] up to the old
+ * length, so that tokens appended there start from 0; positions there are not
+ * written, nor anything past the old length).  `in` and `out` may be the same
+ * buffers, else they must not overlap; with `out` apart, a repeated call
+ * repeats the same moves.
+ * keep_lens: device int32 [num_seqs]; a negative one sets
+ * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole.  The blocks of every
+ * evicted sequence must be private to it (copy them on write first).  All
+ * pool types.  At most 65535 sequences.
+ * workspace: pa_evict_workspace_bytes().
+ */
+pa_status pa_evict_workspace_bytes(const pa_pool* pool, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   int32_t max_context_len, size_t* bytes);
+
+pa_status pa_evict_tokens(const pa_pool* pool, void* k_pool, void* v_pool,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* context_lens, int32_t num_seqs, const int32_t* keep_lens,
+                          int32_t sinks, int32_t recent, const pa_track* in, const pa_track* out,
+                          int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char* pa_last_error(void);

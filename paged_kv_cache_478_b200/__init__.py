@@ -8,7 +8,8 @@ package's directory and must have been built with
 
     python -m paged_kv_cache_478_b200.build
 
-Layouts (see include/pagedattn.h): pools [num_blocks, heads, 16, head_dim];
+Layouts (see include/pagedattn.h): pools [num_blocks, heads, 16, head_dim],
+4-bit pools uint8 [num_blocks, heads, 9 * head_dim];
 q, out, k_new, v_new [tokens or seqs, heads, head_dim]; block_tables int32
 [num_seqs, max_blocks]; context_lens int32 [num_seqs]; slot_mapping int32
 [num_tokens]; pairs int32 [num_pairs, 2].
@@ -21,7 +22,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
 
-PA_F32, PA_F16, PA_BF16 = 0, 1, 2
+PA_F32, PA_F16, PA_BF16, PA_Q4_F16, PA_Q4_BF16 = 0, 1, 2, 3, 4
 PA_OK = 0
 PA_ERR_NO_FREE_BLOCKS = 5
 PA_DEVERR_BLOCK_ID = 0x1
@@ -51,6 +52,15 @@ class pa_pool(ctypes.Structure):
         ("head_stride", ctypes.c_int64),
         ("block_stride", ctypes.c_int64),
         ("bytes_per_pool", ctypes.c_int64),
+    ]
+
+
+class pa_track(ctypes.Structure):
+    _fields_ = [
+        ("mass", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("history", ctypes.c_void_p),
+        ("stride", ctypes.c_int64),
     ]
 
 
@@ -92,6 +102,17 @@ def lib():
             "pa_prefill_attention": [P(pa_pool), vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
                                      ctypes.c_float, vp, vp],
             "pa_copy_blocks": [P(pa_pool), vp, vp, vp, i32, vp],
+            "pa_convert_blocks": [P(pa_pool), vp, vp, P(pa_pool), vp, vp, vp, i32, vp],
+            "pa_decode_mass_workspace_bytes": [P(pa_pool), i32, i32, i32, i32, P(sz)],
+            "pa_decode_attention_mass": [P(pa_pool), vp, vp, vp, vp, i32, vp, i32, i32,
+                                         ctypes.c_float, vp, vp, vp, i64, ctypes.c_float, vp, sz,
+                                         i32, vp],
+            "pa_decode_attention_mass_planned": [P(pa_pool), vp, vp, vp, vp, i32, i32, i32,
+                                                 ctypes.c_float, vp, vp, vp, i64, ctypes.c_float,
+                                                 vp, sz, i32, vp],
+            "pa_evict_workspace_bytes": [P(pa_pool), i32, i32, i32, P(sz)],
+            "pa_evict_tokens": [P(pa_pool), vp, vp, vp, i32, vp, i32, vp, i32, i32, P(pa_track),
+                                P(pa_track), i32, vp, sz, vp],
             "pa_device_errors": [vp, P(ctypes.c_uint32)],
             "pa_selftest_wait_timeout": [vp],
             "pa_alloc_create": [i64, P(vp)],
@@ -165,7 +186,8 @@ def _stream(stream):
 
 
 def pa_pool_create(num_blocks: int, block_size: int, heads: int, head_dim: int, dtype) -> pa_pool:
-    """Describe a pool; dtype is a torch dtype or a PA_* code."""
+    """Describe a pool; dtype is a torch dtype or a PA_* code (PA_Q4_F16 and
+    PA_Q4_BF16: 4-bit pools whose q, out, k_new and v_new are fp16 and bf16)."""
     code = dtype if isinstance(dtype, int) else _dtype_code(dtype)
     p = pa_pool()
     _check(lib().pa_pool_create(num_blocks, block_size, heads, head_dim, code, ctypes.byref(p)))
@@ -184,14 +206,17 @@ def _q_heads(pool: pa_pool) -> int:
 
 def _pool_torch_dtype(pool: pa_pool):
     torch = _torch()
-    return {PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16}[pool.dtype]
+    return {PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16,
+            PA_Q4_F16: torch.float16, PA_Q4_BF16: torch.bfloat16}[pool.dtype]
 
 
 def _check_pool_tensor(pool, t, name):
-    shape = (pool.num_blocks, pool.heads, pool.block_size, pool.head_dim)
+    q4 = pool.dtype in (PA_Q4_F16, PA_Q4_BF16)
+    shape = ((pool.num_blocks, pool.heads, 9 * pool.head_dim) if q4 else
+             (pool.num_blocks, pool.heads, pool.block_size, pool.head_dim))
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _dev_ptr(t, name, _pool_torch_dtype(pool))
+    return _dev_ptr(t, name, _torch().uint8 if q4 else _pool_torch_dtype(pool))
 
 
 def pa_reshape_and_cache(pool, k_new, v_new, slot_mapping, k_pool, v_pool, stream=None):
@@ -419,6 +444,120 @@ def pa_copy_blocks(pool, k_pool, v_pool, pairs, stream=None):
         ctypes.byref(pool), _check_pool_tensor(pool, k_pool, "k_pool"),
         _check_pool_tensor(pool, v_pool, "v_pool"), _dev_ptr(pairs, "pairs", torch.int32), n,
         _stream(stream)))
+
+
+def pa_convert_blocks(src_pool, k_src, v_src, dst_pool, k_dst, v_dst, pairs, stream=None):
+    """Copy whole blocks between a 16-bit pool and a 4-bit one, in either
+    direction; pairs int32 [n, 2] = (block of src_pool, block of dst_pool)."""
+    torch = _torch()
+    n = pairs.shape[0] if pairs.dim() == 2 else pairs.numel() // 2
+    _check(lib().pa_convert_blocks(
+        ctypes.byref(src_pool), _check_pool_tensor(src_pool, k_src, "k_src"),
+        _check_pool_tensor(src_pool, v_src, "v_src"), ctypes.byref(dst_pool),
+        _check_pool_tensor(dst_pool, k_dst, "k_dst"), _check_pool_tensor(dst_pool, v_dst, "v_dst"),
+        _dev_ptr(pairs, "pairs", torch.int32), n, _stream(stream)))
+
+
+def pa_decode_mass_workspace_bytes(pool, num_seqs, max_blocks_per_seq, max_context_len=0,
+                                   partition_size=0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pa_decode_mass_workspace_bytes(ctypes.byref(pool), num_seqs, max_blocks_per_seq,
+                                                max_context_len, partition_size, ctypes.byref(n)))
+    return n.value
+
+
+def _mass_args(S, mass_in, mass_out):
+    torch = _torch()
+    if mass_out.dim() != 2 or mass_out.shape[0] != S:
+        raise ValueError("mass_out must be [num_seqs, tokens]")
+    if mass_in is not None and tuple(mass_in.shape) != tuple(mass_out.shape):
+        raise ValueError("mass_in must have mass_out's shape")
+    return (None if mass_in is None else _dev_ptr(mass_in, "mass_in", torch.float32),
+            _dev_ptr(mass_out, "mass_out", torch.float32), mass_out.shape[1])
+
+
+def pa_decode_attention_mass(pool, q, k_pool, v_pool, block_tables, context_lens, scale, out,
+                             mass_in, mass_out, workspace, decay=1.0, max_context_len=0,
+                             partition_size=0, stream=None):
+    """pa_decode_attention that also writes mass_out[s, t] = decay * mass_in[s,
+    t] + the softmax weight of token t summed over the query heads.  mass_in
+    may be mass_out, or None for zero; both fp32 [num_seqs, tokens]."""
+    torch = _torch()
+    S = q.shape[0]
+    if tuple(q.shape) != (S, _q_heads(pool), pool.head_dim) or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("q and out must be [num_seqs, query heads, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or tuple(context_lens.shape) != (S,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs]")
+    dt = _pool_torch_dtype(pool)
+    m_in, m_out, stride = _mass_args(S, mass_in, mass_out)
+    _check(lib().pa_decode_attention_mass(
+        ctypes.byref(pool), _dev_ptr(q, "q", dt), _check_pool_tensor(pool, k_pool, "k_pool"),
+        _check_pool_tensor(pool, v_pool, "v_pool"),
+        _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32), S, max_context_len, float(scale),
+        _dev_ptr(out, "out", dt), m_in, m_out, stride, float(decay),
+        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        partition_size, _stream(stream)))
+
+
+def pa_decode_attention_mass_planned(pool, q, k_pool, v_pool, block_tables, scale, out, mass_in,
+                                     mass_out, workspace, decay=1.0, max_context_len=0,
+                                     partition_size=0, stream=None):
+    torch = _torch()
+    S = q.shape[0]
+    if tuple(q.shape) != (S, _q_heads(pool), pool.head_dim) or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("q and out must be [num_seqs, query heads, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    dt = _pool_torch_dtype(pool)
+    m_in, m_out, stride = _mass_args(S, mass_in, mass_out)
+    _check(lib().pa_decode_attention_mass_planned(
+        ctypes.byref(pool), _dev_ptr(q, "q", dt), _check_pool_tensor(pool, k_pool, "k_pool"),
+        _check_pool_tensor(pool, v_pool, "v_pool"),
+        _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], S,
+        max_context_len, float(scale), _dev_ptr(out, "out", dt), m_in, m_out, stride, float(decay),
+        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        partition_size, _stream(stream)))
+
+
+def pa_evict_workspace_bytes(pool, num_seqs, max_blocks_per_seq, max_context_len=0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pa_evict_workspace_bytes(ctypes.byref(pool), num_seqs, max_blocks_per_seq,
+                                          max_context_len, ctypes.byref(n)))
+    return n.value
+
+
+def _track(track, S, name):
+    torch = _torch()
+    mass, positions, history = track["mass"], track["positions"], track["history"]
+    if mass.dim() != 2 or mass.shape[0] != S or tuple(positions.shape) != tuple(mass.shape):
+        raise ValueError(f"{name}: mass and positions must be [num_seqs, tokens]")
+    if tuple(history.shape) != (S, 2):
+        raise ValueError(f"{name}: history must be [num_seqs, 2]")
+    return pa_track(_dev_ptr(mass, "mass", torch.float32),
+                    _dev_ptr(positions, "positions", torch.int32),
+                    _dev_ptr(history, "history", torch.int32), mass.shape[1])
+
+
+def pa_evict_tokens(pool, k_pool, v_pool, block_tables, context_lens, keep_lens, sinks, recent,
+                    track, track_out, workspace, max_context_len=0, stream=None):
+    """Evict by gathered weight, in place: of context_lens[s] tokens
+    keep_lens[s] stay, in the sequence's first slots.  track, track_out: dicts
+    of device tensors mass fp32 [S, tokens], positions int32 [S, tokens] and
+    history int32 [S, 2] (all zero for a new sequence); they may be the same."""
+    torch = _torch()
+    S = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or tuple(keep_lens.shape) != (S,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], keep_lens [num_seqs]")
+    t_in, t_out = _track(track, S, "track"), _track(track_out, S, "track_out")
+    _check(lib().pa_evict_tokens(
+        ctypes.byref(pool), _check_pool_tensor(pool, k_pool, "k_pool"),
+        _check_pool_tensor(pool, v_pool, "v_pool"),
+        _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32), S,
+        _dev_ptr(keep_lens, "keep_lens", torch.int32), sinks, recent, ctypes.byref(t_in),
+        ctypes.byref(t_out), max_context_len, _dev_ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def pa_device_errors(stream=None) -> int:

@@ -127,7 +127,8 @@ __device__ __forceinline__ void ring_sync(int r) {
 // max is exact, so the split changes no bit); then lanes < CPR each own one
 // 16-byte output chunk.  Partials are read with .cg loads (L2), since other
 // CTAs wrote them during this launch.  Called by all 32 lanes of the warp.
-template <typename T, int D>
+// MASS: the logarithm of the merged softmax sum is stored too (mass.cuh).
+template <typename T, int D, bool MASS = false>
 __device__ __forceinline__ void merge_partitions(const DecodeArgs& a, int64_t sh, int np, int lane) {
   using C = Chunk<T>;
   constexpr int VEC = C::N;
@@ -158,6 +159,7 @@ __device__ __forceinline__ void merge_partitions(const DecodeArgs& a, int64_t sh
       acc[e + 3] = fmaf(w, x.w, acc[e + 3]);
     }
   }
+  if (MASS && lane == 0) a.lse[sh] = M + log2f(den);
   const float inv = 1.f / den;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] *= inv;
@@ -190,7 +192,7 @@ __device__ __forceinline__ void store_out(T* dst, const float* v) {
 // its order are those of merge_partitions, so the results are the same bits.
 // Returns the number of fills used, negated if a copy did not land in time
 // (nothing is written then).
-template <typename T, int D, int NSTAGE, int BUF>
+template <typename T, int D, int NSTAGE, int BUF, bool MASS = false>
 __device__ __forceinline__ int merge_staged(const DecodeArgs& a, int64_t sh, int np, int lane,
                                             uint8_t* buf, uint64_t* bars, uint32_t fill0) {
   constexpr int ROW = D * 4;                        // one partial row, fp32
@@ -242,6 +244,7 @@ __device__ __forceinline__ int merge_staged(const DecodeArgs& a, int64_t sh, int
     mbar_wait_bounded(smem_addr(&bars[k % NSTAGE]), (k / NSTAGE) & 1u);  // let the copy land
     return -used;
   }
+  if (MASS && lane == 0) a.lse[sh] = M + log2f(den);
   const float inv = 1.f / den;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) acc[e] *= inv;
@@ -253,8 +256,9 @@ __device__ __forceinline__ int merge_staged(const DecodeArgs& a, int64_t sh, int
 // The persistent partition kernel: CTAs pull (sequence, partition, head
 // group) items from the plan's queue.  Each ring of G warps streams one KV
 // head of the item through NSTAGE stages of bulk copies; each warp of the
-// ring attends with its own query head (G == 1: one warp per head).
-template <typename T, int D, int WARPS, int NSTAGE, int G>
+// ring attends with its own query head (G == 1: one warp per head).  MASS: the
+// scores and the softmax sums' logarithms are stored for mass.cuh.
+template <typename T, int D, int WARPS, int NSTAGE, int G, bool MASS>
 __global__ void __launch_bounds__(WARPS * 32) paged_decode_kernel(DecodeArgs a) {
   using Cfg = DecodeConfig<T, D, WARPS, NSTAGE, G>;
   using C = Chunk<T>;
@@ -415,6 +419,10 @@ __global__ void __launch_bounds__(WARPS * 32) paged_decode_kernel(DecodeArgs a) 
         }
         halve<CPR / 2, NCH>(part, lane);
         float sc = part[0] + __shfl_xor_sync(kFullMask, part[0], 1);
+        if constexpr (MASS) {  // two lanes hold each score
+          if ((lane & 1) == 0 && my_row < valid)
+            a.scores[sh * a.score_stride + tok0 + i * kBlock + my_row] = sc;
+        }
         if (my_row >= valid) sc = -INFINITY;
 
         float bmax = sc;
@@ -482,6 +490,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_decode_kernel(DecodeArgs a) 
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = l_run > 0.f ? acc[e] * inv : 0.f;
             reinterpret_cast<uint4*>(static_cast<T*>(a.out) + sh * D)[c] = C::from_float(o);
+            if (MASS && lane == 0) a.lse[sh] = m_run + log2f(l_run);
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part_acc + (sh * a.max_parts + p) * D + c * VEC);
 #pragma unroll
@@ -517,7 +526,8 @@ __global__ void __launch_bounds__(WARPS * 32) paged_decode_kernel(DecodeArgs a) 
           // one query head per ring: the partials come through the warp's ring
           constexpr int BUF = NSTAGE * Cfg::STAGE_BYTES;
           const int used =
-              merge_staged<T, D, NSTAGE, BUF>(a, (int64_t)s * HQ + hq, np, lane, my_stages, my_bars, fills);
+              merge_staged<T, D, NSTAGE, BUF, MASS>(a, (int64_t)s * HQ + hq, np, lane, my_stages,
+                                                    my_bars, fills);
           fills += used > 0 ? used : -used;
           if (used < 0 && lane == 0) {  // as for a copy of the item: report, stop, poison the plan
             atomicOr(a.err, PA_DEVERR_TIMEOUT);
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_decode_kernel(DecodeArgs a) 
             __threadfence();
           }
         } else {
-          merge_partitions<T, D>(a, (int64_t)s * HQ + hq, np, lane);
+          merge_partitions<T, D, MASS>(a, (int64_t)s * HQ + hq, np, lane);
         }
       }
     }

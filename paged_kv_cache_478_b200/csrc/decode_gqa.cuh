@@ -77,7 +77,7 @@ struct GqaConfig {
 // those of merge_partitions (max over the partitions, then the weighted sums
 // in partition order), so the results are the same bits.  Returns false if
 // a copy did not land in time (nothing is written then).
-template <typename T, int D, int G, int NSTAGE, int BUF>
+template <typename T, int D, int G, int NSTAGE, int BUF, bool MASS = false>
 __device__ __forceinline__ bool merge_group(const DecodeArgs& a, int64_t sh0, int np, int lane,
                                             uint8_t* buf, uint64_t* bars, uint32_t& fills) {
   constexpr int LPH = 32 / G;        // lanes per query head
@@ -160,6 +160,7 @@ __device__ __forceinline__ bool merge_group(const DecodeArgs& a, int64_t sh0, in
     mbar_wait_bounded(smem_addr(&bars[k % NSTAGE]), (k / NSTAGE) & 1u);  // let the copies land
     return false;
   }
+  if (MASS && cl == 0) a.lse[sh] = M + log2f(den);
   const float inv = 1.f / den;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) acc[e] *= inv;
@@ -173,8 +174,9 @@ __device__ __forceinline__ bool merge_group(const DecodeArgs& a, int64_t sh0, in
 }
 
 // tm_k, tm_v: the K and V pools as [num_blocks * heads * 16 rows][head_dim],
-// box {64, 16}, 128-byte swizzle.
-template <typename T, int D, int NSTAGE>
+// box {64, 16}, 128-byte swizzle.  MASS: the scores and the softmax sums'
+// logarithms are stored for mass.cuh.
+template <typename T, int D, int NSTAGE, bool MASS>
 __global__ void __launch_bounds__(128, 3)  // 3 CTAs per SM: at most 168 registers a thread
     paged_decode_gqa_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
@@ -365,6 +367,16 @@ __global__ void __launch_bounds__(128, 3)  // 3 CTAs per SM: at most 168 registe
         float x1 = t0 + 1 < valid ? sc[0][1] * a.scale_log2 : -INFINITY;
         float x2 = t0 + 8 < valid ? sc[1][0] * a.scale_log2 : -INFINITY;
         float x3 = t0 + 9 < valid ? sc[1][1] * a.scale_log2 : -INFINITY;
+        if constexpr (MASS) {
+          if (row_ok) {
+            float* dst = a.scores + ((int64_t)s * HQ + kvh * G + qrow) * a.score_stride + tok0 +
+                         (jb + i) * kBlock;
+            if (t0 < valid) dst[t0] = x0;
+            if (t0 + 1 < valid) dst[t0 + 1] = x1;
+            if (t0 + 8 < valid) dst[t0 + 8] = x2;
+            if (t0 + 9 < valid) dst[t0 + 9] = x3;
+          }
+        }
         float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
         mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
@@ -481,6 +493,7 @@ __global__ void __launch_bounds__(128, 3)  // 3 CTAs per SM: at most 168 registe
             const uint32_t v = MmaType<T>::pack(o[j][0] * inv, o[j][1] * inv);
             *reinterpret_cast<uint32_t*>(dst + j * 8) = v;
           }
+          if (MASS && (lane & 3) == 0) a.lse[sh] = m_run + log2f(l_run);
         } else {
           float* dst = a.part_acc + (sh * a.max_parts + p) * D + d0;
 #pragma unroll
@@ -505,11 +518,11 @@ __global__ void __launch_bounds__(128, 3)  // 3 CTAs per SM: at most 168 registe
         __threadfence();
         constexpr int BUF = NSTAGE * Cfg::STAGE_BYTES;
         const bool merged =
-            G == 8   ? merge_group<T, D, 8, NSTAGE, BUF>(a, (int64_t)s * HQ + kvh * G, np, lane,
+            G == 8   ? merge_group<T, D, 8, NSTAGE, BUF, MASS>(a, (int64_t)s * HQ + kvh * G, np, lane,
                                                          my_stages, my_bars, fills)
-            : G == 4 ? merge_group<T, D, 4, NSTAGE, BUF>(a, (int64_t)s * HQ + kvh * G, np, lane,
+            : G == 4 ? merge_group<T, D, 4, NSTAGE, BUF, MASS>(a, (int64_t)s * HQ + kvh * G, np, lane,
                                                          my_stages, my_bars, fills)
-                     : merge_group<T, D, 2, NSTAGE, BUF>(a, (int64_t)s * HQ + kvh * G, np, lane,
+                     : merge_group<T, D, 2, NSTAGE, BUF, MASS>(a, (int64_t)s * HQ + kvh * G, np, lane,
                                                          my_stages, my_bars, fills);
         if (!merged && lane == 0) {  // as for a copy of the item: report, stop, poison the plan
           atomicOr(a.err, PA_DEVERR_TIMEOUT);

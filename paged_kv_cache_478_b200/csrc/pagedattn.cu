@@ -20,6 +20,10 @@
 #include "shared_prefix.cuh"
 #include "decode_gqa.cuh"
 #include "prefill.cuh"
+#include "quant4.cuh"
+#include "decode_q4.cuh"
+#include "mass.cuh"
+#include "evict.cuh"
 #include "pagedattn.h"
 #include "status.h"
 
@@ -91,14 +95,20 @@ template <typename T, int D, int G>
 using DecodeKernelCfg =
     DecodeConfig<T, D, warps_for(G), stages_for(kBlock * D * (int)sizeof(T), G), G>;
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool MASS = false>
 constexpr auto decode_kernel_ptr() {
-  return paged_decode_kernel<T, D, warps_for(G), stages_for(kBlock * D * (int)sizeof(T), G), G>;
+  return paged_decode_kernel<T, D, warps_for(G), stages_for(kBlock * D * (int)sizeof(T), G), G, MASS>;
 }
 
 template <typename T, int D, int G>
 cudaError_t set_decode_attrs() {
   const size_t smem = DecodeKernelCfg<T, D, G>::smem_bytes(kMaxPartition);
+  // fp16 and bf16 pools with grouped queries never reach this kernel (use_gqa_mma)
+  if constexpr (G == 1 || sizeof(T) == 4) {
+    const cudaError_t e = cudaFuncSetAttribute(decode_kernel_ptr<T, D, G, true>(),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return cudaFuncSetAttribute(decode_kernel_ptr<T, D, G>(),
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
@@ -120,13 +130,24 @@ int rings_for(int G) { return warps_for(G) / G; }
 // kernel.  (Pairs once ran faster on CUDA cores; since the tensor-core
 // kernel stages whole tiles and merges all heads of a KV head at once it
 // is faster for them too: 106 -> 89 us on 200 requests x 8 KV heads.)
-bool use_gqa_mma(const pa_pool* pool) { return pool->q_per_kv >= 2 && pool->dtype != PA_F32; }
+bool is_q4(const pa_pool* pool) { return pool->dtype == PA_Q4_F16 || pool->dtype == PA_Q4_BF16; }
+
+bool use_gqa_mma(const pa_pool* pool) {
+  return pool->q_per_kv >= 2 && (pool->dtype == PA_F16 || pool->dtype == PA_BF16);
+}
 #ifndef PA_GQA_STAGES
 #define PA_GQA_STAGES 2
 #endif
 constexpr int kGqaStages = PA_GQA_STAGES;  // per-warp ring depth of the tensor-core kernel
 
+// Bytes of one physical block of a K or V pool.
+int64_t block_bytes(const pa_pool* pool) {
+  return is_q4(pool) ? (int64_t)pool->heads * q4_tile_bytes(pool->head_dim)
+                     : (int64_t)pool->heads * kBlock * pool->head_dim * pool->elem_bytes;
+}
+
 int kv_heads_per_item(const pa_pool* pool) {
+  if (is_q4(pool)) return Q4Config<__half, 128>::KVPI;
   return use_gqa_mma(pool) ? GqaConfig<__half, 128, kGqaStages>::KVPI : rings_for(pool->q_per_kv);
 }
 
@@ -208,9 +229,12 @@ cudaError_t set_shared_prefix_attrs() {
 
 template <typename T, int D>
 cudaError_t set_gqa_attrs() {
-  return cudaFuncSetAttribute(paged_decode_gqa_kernel<T, D, kGqaStages>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)GqaConfig<T, D, kGqaStages>::smem_bytes(kMaxPartition));
+  const int smem = (int)GqaConfig<T, D, kGqaStages>::smem_bytes(kMaxPartition);
+  const cudaError_t e = cudaFuncSetAttribute(paged_decode_gqa_kernel<T, D, kGqaStages, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_decode_gqa_kernel<T, D, kGqaStages, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 // Launch a persistent decode kernel.  With `overlap`, it is a programmatic
@@ -242,7 +266,8 @@ template <typename T, int D>
 cudaError_t launch_gqa(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream,
                        const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool overlap = false) {
   using Cfg = GqaConfig<T, D, kGqaStages>;
-  auto kernel = paged_decode_gqa_kernel<T, D, kGqaStages>;
+  auto kernel = a.scores ? paged_decode_gqa_kernel<T, D, kGqaStages, true>
+                         : paged_decode_gqa_kernel<T, D, kGqaStages, false>;
   const size_t smem = Cfg::smem_bytes(a.partition_size);
   int per_sm = 0;
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);
@@ -315,7 +340,7 @@ pa_status check_pool(const pa_pool* pool) {
   if (pool->block_size != kBlock) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16");
   if (pool->head_dim != 64 && pool->head_dim != 128)
     return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
-  if (pool->dtype < PA_F32 || pool->dtype > PA_BF16) return fail(PA_ERR_UNSUPPORTED, "unknown dtype");
+  if (pool->dtype < PA_F32 || pool->dtype > PA_Q4_BF16) return fail(PA_ERR_UNSUPPORTED, "unknown dtype");
   if (pool->q_per_kv != 1 && pool->q_per_kv != 2 && pool->q_per_kv != 4 && pool->q_per_kv != 8)
     return fail(PA_ERR_UNSUPPORTED, "query heads per KV head must be 1, 2, 4 or 8");
   if (pool->num_blocks <= 0 || pool->heads <= 0) return fail(PA_ERR_INVALID_ARG, "empty pool");
@@ -367,6 +392,22 @@ WorkspaceLayout layout_for(int64_t S, int64_t H, int64_t max_parts, int64_t D, i
   return w;
 }
 
+// Scores and softmax sums of a weight-gathering call, behind the decode
+// workspace (offsets from its end, which is 256-byte aligned).
+struct MassLayout {
+  size_t lse = 0, scores = 0, total = 0;
+  int64_t stride = 0;  // tokens between query heads
+};
+
+MassLayout mass_layout(const pa_pool* pool, int64_t S, int maxL) {
+  MassLayout m;
+  const int64_t rows = S * pool->heads * pool->q_per_kv;
+  m.stride = ((int64_t)maxL + 3) / 4 * 4;
+  m.scores = align256(rows * 4);
+  m.total = align256(m.scores + rows * m.stride * 4);
+  return m;
+}
+
 int round_up16(int64_t x) { return (int)std::min<int64_t>(kMaxPartition, (x + 15) / 16 * 16); }
 
 // Automatic partition size.  Every work item pays a pipeline ramp and a
@@ -401,6 +442,22 @@ cudaError_t launch_decode(const DecodeArgs& a, const DeviceState& dev, cudaStrea
                           bool overlap = false) {
   using Cfg = DecodeKernelCfg<T, D, G>;
   auto kernel = decode_kernel_ptr<T, D, G>();
+  if constexpr (G == 1 || sizeof(T) == 4)
+    if (a.scores) kernel = decode_kernel_ptr<T, D, G, true>();
+  const size_t smem = Cfg::smem_bytes(a.partition_size);
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);
+  if (e != cudaSuccess) return e;
+  per_sm = std::max(per_sm, 1);
+  const int64_t upper = (int64_t)a.num_seqs * a.max_parts * a.head_groups;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(upper, (int64_t)dev.num_sms * per_sm));
+  return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap);
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream, bool overlap) {
+  using Cfg = Q4Config<T, D>;
+  auto kernel = a.scores ? paged_decode_q4_kernel<T, D, G, true> : paged_decode_q4_kernel<T, D, G, false>;
   const size_t smem = Cfg::smem_bytes(a.partition_size);
   int per_sm = 0;
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);
@@ -412,6 +469,17 @@ cudaError_t launch_decode(const DecodeArgs& a, const DeviceState& dev, cudaStrea
 }
 
 template <typename T, int D>
+cudaError_t launch_q4_grouped(int G, const DecodeArgs& a, const DeviceState& dev, cudaStream_t s,
+                              bool overlap) {
+  switch (G) {
+    case 1: return launch_q4<T, D, 1>(a, dev, s, overlap);
+    case 2: return launch_q4<T, D, 2>(a, dev, s, overlap);
+    case 4: return launch_q4<T, D, 4>(a, dev, s, overlap);
+    default: return launch_q4<T, D, 8>(a, dev, s, overlap);
+  }
+}
+
+template <typename T, int D>
 cudaError_t launch_grouped(int G, const DecodeArgs& a, const DeviceState& dev, cudaStream_t s,
                            bool overlap = false) {
   switch (G) {
@@ -420,6 +488,26 @@ cudaError_t launch_grouped(int G, const DecodeArgs& a, const DeviceState& dev, c
     case 4: return launch_decode<T, D, 4>(a, dev, s, overlap);
     default: return launch_decode<T, D, 8>(a, dev, s, overlap);
   }
+}
+
+// Quantise new tokens into a 4-bit pool: eight lanes per (token, head, 64 dimensions).
+pa_status launch_q4_append(const DeviceState& dev, const pa_pool* pool, const void* k_new,
+                           const void* v_new, const int32_t* slots, int32_t num_tokens, void* k_pool,
+                           void* v_pool, cudaStream_t s) {
+  const int64_t threads = (int64_t)num_tokens * pool->heads * (pool->head_dim / 64) * 8;
+  const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev.num_sms * 8);
+  auto kp = static_cast<uint8_t*>(k_pool), vp = static_cast<uint8_t*>(v_pool);
+  const int64_t num_slots = pool->num_blocks * pool->block_size;
+  if (pool->dtype == PA_Q4_BF16)
+    q4_append_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(k_new),
+                                          static_cast<const __nv_bfloat16*>(v_new), slots, kp, vp,
+                                          pool->heads, pool->head_dim, num_tokens, num_slots, dev.err);
+  else
+    q4_append_kernel<<<grid, 256, 0, s>>>(static_cast<const __half*>(k_new),
+                                          static_cast<const __half*>(v_new), slots, kp, vp,
+                                          pool->heads, pool->head_dim, num_tokens, num_slots, dev.err);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "4-bit append launch");
 }
 
 // One warp waits on a barrier that expects two arrivals but gets one.
@@ -462,6 +550,12 @@ pa_status pa_pool_create(int64_t num_blocks, int32_t block_size, int32_t heads, 
   p.head_stride = (int64_t)block_size * head_dim;
   p.block_stride = (int64_t)heads * block_size * head_dim;
   p.bytes_per_pool = num_blocks * p.block_stride * p.elem_bytes;
+  if (is_q4(&p)) {  // strides in bytes: 16-byte pieces of a token, tiles, blocks
+    p.token_stride = 16;
+    p.head_stride = q4_tile_bytes(head_dim);
+    p.block_stride = heads * p.head_stride;
+    p.bytes_per_pool = num_blocks * p.block_stride;
+  }
   pa_status st = check_pool(&p);
   if (st != PA_OK) return st;
   *out = p;
@@ -494,6 +588,9 @@ pa_status pa_reshape_and_cache(const pa_pool* pool, const void* k_new, const voi
     return fail(PA_ERR_INVALID_ARG, "pa_reshape_and_cache: buffers must be 16-byte aligned");
   DeviceState* dev;
   if ((st = device_state(&dev)) != PA_OK) return st;
+  if (is_q4(pool))
+    return launch_q4_append(*dev, pool, k_new, v_new, slot_mapping, num_tokens, k_pool, v_pool,
+                            static_cast<cudaStream_t>(stream));
   const int row_chunks = pool->head_dim * pool->elem_bytes / 16;
   const int64_t total = (int64_t)num_tokens * pool->heads * row_chunks;
   const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)dev->num_sms * 16);
@@ -526,6 +623,20 @@ pa_status pa_decode_shared_prefix_workspace_bytes(const pa_pool* pool, int32_t n
   return PA_OK;
 }
 
+pa_status pa_decode_mass_workspace_bytes(const pa_pool* pool, int32_t num_seqs,
+                                         int32_t max_blocks_per_seq, int32_t max_context_len,
+                                         int32_t partition_size, size_t* bytes) {
+  size_t base = 0;
+  if (!bytes) return fail(PA_ERR_INVALID_ARG, "workspace bytes: bytes is null");
+  pa_status st = pa_decode_workspace_bytes(pool, num_seqs, max_blocks_per_seq, max_context_len,
+                                           partition_size, &base);
+  if (st != PA_OK) return st;
+  *bytes = base + mass_layout(pool, num_seqs,
+                              resolve_max_context(pool, max_blocks_per_seq, max_context_len))
+                      .total;
+  return PA_OK;
+}
+
 pa_status pa_decode_workspace_bytes(const pa_pool* pool, int32_t num_seqs,
                                     int32_t max_blocks_per_seq, int32_t max_context_len,
                                     int32_t partition_size, size_t* bytes) {
@@ -542,7 +653,7 @@ namespace {
 pa_status prepare_decode(const pa_pool* pool, int32_t num_seqs, int32_t max_blocks_per_seq,
                          int32_t max_context_len, int32_t partition_size, void* workspace,
                          size_t workspace_bytes, DecodeArgs* a, DeviceState** dev,
-                         int32_t max_shared_blocks = 0) {
+                         int32_t max_shared_blocks = 0, bool mass = false) {
   pa_status st = check_pool(pool);
   if (st != PA_OK) return st;
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
@@ -568,7 +679,9 @@ pa_status prepare_decode(const pa_pool* pool, int32_t num_seqs, int32_t max_bloc
   const int max_parts = total_parts(maxL, ps, max_shared_blocks);
   const WorkspaceLayout w = layout_for(num_seqs, (int64_t)pool->heads * G, max_parts,
                                        pool->head_dim, G, kv_heads_per_item(pool));
-  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const MassLayout ml = mass ? mass_layout(pool, num_seqs, maxL) : MassLayout{};
+  if (!workspace || workspace_bytes < w.total + ml.total ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(PA_ERR_WORKSPACE, "decode: workspace missing, not 256-byte aligned or too small");
   char* ws = static_cast<char*>(workspace);
   *a = DecodeArgs{};
@@ -584,6 +697,11 @@ pa_status prepare_decode(const pa_pool* pool, int32_t num_seqs, int32_t max_bloc
   a->part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   a->part_acc = reinterpret_cast<float*>(ws + w.part_acc);
   a->merge_cnt = reinterpret_cast<int32_t*>(ws + w.merge_cnt);
+  if (mass) {
+    a->lse = reinterpret_cast<float*>(ws + w.total + ml.lse);
+    a->scores = reinterpret_cast<float*>(ws + w.total + ml.scores);
+    a->score_stride = ml.stride;
+  }
   a->err = (*dev)->err;
   a->num_blocks = pool->num_blocks;
   a->max_blocks_per_seq = max_blocks_per_seq;
@@ -702,6 +820,14 @@ pa_status launch_run(const pa_pool* pool, const DecodeArgs& a, const DeviceState
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode launch");
   }
   switch (pool->dtype * 1000 + pool->head_dim) {
+    case PA_Q4_F16 * 1000 + 64: e = launch_q4_grouped<__half, 64>(pool->q_per_kv, a, dev, s, overlap); break;
+    case PA_Q4_F16 * 1000 + 128: e = launch_q4_grouped<__half, 128>(pool->q_per_kv, a, dev, s, overlap); break;
+    case PA_Q4_BF16 * 1000 + 64:
+      e = launch_q4_grouped<__nv_bfloat16, 64>(pool->q_per_kv, a, dev, s, overlap);
+      break;
+    case PA_Q4_BF16 * 1000 + 128:
+      e = launch_q4_grouped<__nv_bfloat16, 128>(pool->q_per_kv, a, dev, s, overlap);
+      break;
     case PA_F32 * 1000 + 64: e = launch_grouped<float, 64>(pool->q_per_kv, a, dev, s, overlap); break;
     case PA_F32 * 1000 + 128: e = launch_grouped<float, 128>(pool->q_per_kv, a, dev, s, overlap); break;
     case PA_F16 * 1000 + 64: e = launch_grouped<__half, 64>(pool->q_per_kv, a, dev, s, overlap); break;
@@ -713,6 +839,22 @@ pa_status launch_run(const pa_pool* pool, const DecodeArgs& a, const DeviceState
     default: return fail(PA_ERR_UNSUPPORTED, "decode: dtype/head_dim not built");
   }
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode launch");
+}
+
+// Quantise each sequence's new token into the slot of its last position, from
+// the plan's lengths, before the attention of the same call reads it.
+pa_status launch_q4_append_last(const DeviceState& dev, const pa_pool* pool, const DecodeArgs& a,
+                                const void* k_new, const void* v_new, cudaStream_t s) {
+  const int64_t threads = (int64_t)a.num_seqs * pool->heads * (pool->head_dim / 64) * 8;
+  const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev.num_sms * 8);
+  if (pool->dtype == PA_Q4_BF16)
+    q4_append_last_kernel<<<grid, 256, 0, s>>>(a, static_cast<const __nv_bfloat16*>(k_new),
+                                               static_cast<const __nv_bfloat16*>(v_new), pool->head_dim);
+  else
+    q4_append_last_kernel<<<grid, 256, 0, s>>>(a, static_cast<const __half*>(k_new),
+                                               static_cast<const __half*>(v_new), pool->head_dim);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "4-bit append launch");
 }
 
 pa_status check_run_pointers(const void* q, const void* k_pool, const void* v_pool,
@@ -822,6 +964,11 @@ pa_status pa_decode_append_attention_planned(const pa_pool* pool, const void* q,
   if (st != PA_OK) return st;
   if ((st = check_plan(pool, &a, "pa_decode_append_attention_planned")) != PA_OK) return st;
   set_run_args(&a, q, k_pool, v_pool, block_tables, out, scale);
+  if (is_q4(pool)) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = launch_q4_append_last(*dev, pool, a, k_new, v_new, s)) != PA_OK) return st;
+    return launch_run(pool, a, *dev, s);
+  }
   a.k_new = k_new;
   a.v_new = v_new;
   return launch_run(pool, a, *dev, static_cast<cudaStream_t>(stream));
@@ -852,6 +999,10 @@ pa_status pa_decode_append_attention(const pa_pool* pool, const void* q, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = launch_plan(pool, &a, s)) != PA_OK) return st;
   set_run_args(&a, q, k_pool, v_pool, block_tables, out, scale);
+  if (is_q4(pool)) {
+    if ((st = launch_q4_append_last(*dev, pool, a, k_new, v_new, s)) != PA_OK) return st;
+    return launch_run(pool, a, *dev, s);
+  }
   a.k_new = k_new;
   a.v_new = v_new;
   a.after_plan = 1;  // the decode launch overlaps the plan kernel's run
@@ -872,7 +1023,7 @@ pa_status pa_decode_attention_shared_prefix(
   if (num_seqs == 0) return check_pool(pool);
   pa_status st = check_pool(pool);
   if (st != PA_OK) return st;
-  if (pool->dtype == PA_F32)
+  if (pool->dtype != PA_F16 && pool->dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "shared prefix: fp16 or bf16 pools only (tensor-core path)");
   st = check_run_pointers(q, k_pool, v_pool, block_tables, out, scale);
   if (st != PA_OK) return st;
@@ -945,8 +1096,10 @@ pa_status pa_prefill_attention(const pa_pool* pool, const void* q, const void* k
       max_context_len < 0)
     return fail(PA_ERR_INVALID_ARG, "prefill: bad size");
   if (num_seqs == 0 || max_new_tokens == 0 || num_tokens == 0) return PA_OK;
-  if (pool->dtype == PA_F32)
-    return fail(PA_ERR_UNSUPPORTED, "prefill: fp16 or bf16 pools only (tcgen05 kind::f16)");
+  if (pool->dtype != PA_F16 && pool->dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED,
+                "prefill: fp16 or bf16 pools only (tcgen05 kind::f16; pa_convert_blocks reads 4-bit "
+                "blocks back)");
   st = check_run_pointers(q, k_pool, v_pool, block_tables, out, scale);
   if (st != PA_OK) return st;
   if (!context_lens || !query_start) return fail(PA_ERR_INVALID_ARG, "prefill: null pointer");
@@ -1012,7 +1165,7 @@ pa_status pa_copy_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const 
     return fail(PA_ERR_INVALID_ARG, "pa_copy_blocks: pools must be 16-byte aligned");
   DeviceState* dev;
   if ((st = device_state(&dev)) != PA_OK) return st;
-  const int64_t block_chunks = pool->block_stride * pool->elem_bytes / 16;
+  const int64_t block_chunks = block_bytes(pool) / 16;
   const int64_t total = (int64_t)num_pairs * block_chunks;
   const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)dev->num_sms * 16);
   copy_blocks_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
@@ -1020,6 +1173,225 @@ pa_status pa_copy_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const 
       pool->num_blocks, block_chunks, dev->err);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "copy_blocks launch");
+}
+
+pa_status pa_convert_blocks(const pa_pool* src, const void* k_src, const void* v_src,
+                            const pa_pool* dst, void* k_dst, void* v_dst, const int32_t* pairs,
+                            int32_t num_pairs, void* stream) {
+  CallRange range("pa_convert_blocks");
+  pa_status st = check_pool(src);
+  if (st != PA_OK || (st = check_pool(dst)) != PA_OK) return st;
+  if (src->heads != dst->heads || src->head_dim != dst->head_dim)
+    return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: the pools differ in heads or head_dim");
+  const bool pack = is_q4(dst);
+  const pa_pool* wide = pack ? src : dst;
+  const pa_pool* narrow = pack ? dst : src;
+  if (!((wide->dtype == PA_F16 && narrow->dtype == PA_Q4_F16) ||
+        (wide->dtype == PA_BF16 && narrow->dtype == PA_Q4_BF16)))
+    return fail(PA_ERR_UNSUPPORTED,
+                "pa_convert_blocks: one pool is fp16 or bf16, the other 4-bit of the same type");
+  if (num_pairs < 0) return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: num_pairs < 0");
+  if (num_pairs == 0) return PA_OK;
+  if (!k_src || !v_src || !k_dst || !v_dst || !pairs)
+    return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: null pointer");
+  if (!aligned16(k_src) || !aligned16(v_src) || !aligned16(k_dst) || !aligned16(v_dst))
+    return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: pools must be 16-byte aligned");
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != PA_OK) return st;
+  const int64_t threads = (int64_t)num_pairs * src->heads * (src->head_dim / 64) * kBlock * 8;
+  const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev->num_sms * 8);
+  auto kernel = src->dtype == PA_F16       ? q4_convert_kernel<__half, true>
+                : src->dtype == PA_BF16    ? q4_convert_kernel<__nv_bfloat16, true>
+                : src->dtype == PA_Q4_F16  ? q4_convert_kernel<__half, false>
+                                           : q4_convert_kernel<__nv_bfloat16, false>;
+  kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(k_src), static_cast<const uint8_t*>(v_src),
+      static_cast<uint8_t*>(k_dst), static_cast<uint8_t*>(v_dst), pairs, num_pairs, src->num_blocks,
+      dst->num_blocks, src->heads, src->head_dim, dev->err);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "convert_blocks launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+pa_status check_mass(const float* mass_out, int64_t stride, float decay, int maxL) {
+  if (!mass_out) return fail(PA_ERR_INVALID_ARG, "decode mass: mass_out is null");
+  if (stride < maxL)
+    return fail(PA_ERR_INVALID_ARG, "decode mass: mass_stride is below the longest context");
+  if (!std::isfinite(decay)) return fail(PA_ERR_INVALID_ARG, "decode mass: decay not finite");
+  return PA_OK;
+}
+
+pa_status launch_mass(const DecodeArgs& a, const MassArgs& m, cudaStream_t s) {
+  if (a.max_context_len == 0) return PA_OK;
+  if (a.num_seqs > 65535)
+    return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
+  const dim3 grid((unsigned)((a.max_context_len + 255) / 256), (unsigned)a.num_seqs);
+  mass_kernel<<<grid, 256, 0, s>>>(a, m);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "mass launch");
+}
+
+// One call: validate, plan unless planned, decode with the scores stored, gather.
+pa_status decode_mass(const pa_pool* pool, const void* q, const void* k_pool, const void* v_pool,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* context_lens, bool planned, int32_t num_seqs,
+                      int32_t max_context_len, float scale, void* out, const float* mass_in,
+                      float* mass_out, int64_t mass_stride, float decay, void* workspace,
+                      size_t workspace_bytes, int32_t partition_size, cudaStream_t s) {
+  if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "decode mass: num_seqs < 0");
+  if (num_seqs == 0) return check_pool(pool);
+  if (num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
+  pa_status st = check_run_pointers(q, k_pool, v_pool, block_tables, out, scale);
+  if (st != PA_OK) return st;
+  if (!planned && !context_lens) return fail(PA_ERR_INVALID_ARG, "decode mass: context_lens is null");
+  if ((st = check_pool(pool)) != PA_OK) return st;
+  if (max_blocks_per_seq <= 0 || max_context_len < 0)
+    return fail(PA_ERR_INVALID_ARG, "decode: bad size");
+  st = check_mass(mass_out, mass_stride, decay,
+                  resolve_max_context(pool, max_blocks_per_seq, max_context_len));
+  if (st != PA_OK) return st;
+  DecodeArgs a;
+  DeviceState* dev;
+  st = prepare_decode(pool, num_seqs, max_blocks_per_seq, max_context_len, partition_size, workspace,
+                      workspace_bytes, &a, &dev, 0, true);
+  if (st != PA_OK) return st;
+  set_run_args(&a, q, k_pool, v_pool, block_tables, out, scale);
+  if (planned) {
+    if ((st = check_plan(pool, &a, "pa_decode_attention_mass_planned")) != PA_OK) return st;
+  } else {
+    a.context_lens = context_lens;
+    if ((st = launch_plan(pool, &a, s)) != PA_OK) return st;
+    a.after_plan = 1;
+  }
+  if ((st = launch_run(pool, a, *dev, s, !planned)) != PA_OK) return st;
+  return launch_mass(a, MassArgs{mass_in, mass_out, mass_stride, decay}, s);
+}
+
+struct EvictLayout {
+  size_t counts = 0, moves = 0, total = 0;
+  int64_t cap = 0;  // moves of one sequence: at most half of its tokens
+};
+
+EvictLayout evict_layout(int64_t S, int maxL) {
+  EvictLayout e;
+  e.cap = std::max(1, maxL / 2);
+  e.moves = align256(S * 4);
+  e.total = align256(e.moves + S * e.cap * 8);
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_decode_attention_mass(const pa_pool* pool, const void* q, const void* k_pool,
+                                   const void* v_pool, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                   int32_t num_seqs, int32_t max_context_len, float scale, void* out,
+                                   const float* mass_in, float* mass_out, int64_t mass_stride,
+                                   float decay, void* workspace, size_t workspace_bytes,
+                                   int32_t partition_size, void* stream) {
+  CallRange range("pa_decode_attention_mass");
+  return decode_mass(pool, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens, false,
+                     num_seqs, max_context_len, scale, out, mass_in, mass_out, mass_stride, decay,
+                     workspace, workspace_bytes, partition_size, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_decode_attention_mass_planned(const pa_pool* pool, const void* q, const void* k_pool,
+                                           const void* v_pool, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, int32_t num_seqs,
+                                           int32_t max_context_len, float scale, void* out,
+                                           const float* mass_in, float* mass_out,
+                                           int64_t mass_stride, float decay, void* workspace,
+                                           size_t workspace_bytes, int32_t partition_size,
+                                           void* stream) {
+  CallRange range("pa_decode_attention_mass_planned");
+  return decode_mass(pool, q, k_pool, v_pool, block_tables, max_blocks_per_seq, nullptr, true,
+                     num_seqs, max_context_len, scale, out, mass_in, mass_out, mass_stride, decay,
+                     workspace, workspace_bytes, partition_size, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_evict_workspace_bytes(const pa_pool* pool, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   int32_t max_context_len, size_t* bytes) {
+  pa_status st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (!bytes) return fail(PA_ERR_INVALID_ARG, "workspace bytes: bytes is null");
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
+    return fail(PA_ERR_INVALID_ARG, "workspace bytes: bad size");
+  *bytes = evict_layout(num_seqs, resolve_max_context(pool, max_blocks_per_seq, max_context_len)).total;
+  return PA_OK;
+}
+
+pa_status pa_evict_tokens(const pa_pool* pool, void* k_pool, void* v_pool,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* context_lens, int32_t num_seqs, const int32_t* keep_lens,
+                          int32_t sinks, int32_t recent, const pa_track* in, const pa_track* out,
+                          int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  CallRange range("pa_evict_tokens");
+  pa_status st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || sinks < 0 || recent < 0)
+    return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: bad size");
+  if (num_seqs == 0) return PA_OK;
+  if (num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: more than 65535 sequences");
+  if (!k_pool || !v_pool || !block_tables || !context_lens || !keep_lens || !in || !out ||
+      !in->mass || !in->positions || !in->history || !out->mass || !out->positions || !out->history)
+    return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: null pointer");
+  if (!aligned16(k_pool) || !aligned16(v_pool))
+    return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: pools must be 16-byte aligned");
+  const int maxL = resolve_max_context(pool, max_blocks_per_seq, max_context_len);
+  if (in->stride < maxL || out->stride < maxL)
+    return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: a track's stride is below the longest context");
+  if ((in->mass == out->mass || in->positions == out->positions) && in->stride != out->stride)
+    return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: a track in place keeps its stride");
+  const EvictLayout w = evict_layout(num_seqs, maxL);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(PA_ERR_WORKSPACE,
+                "pa_evict_tokens: workspace missing, not 256-byte aligned or too small");
+  DeviceState* dev;
+  if ((st = device_state(&dev)) != PA_OK) return st;
+  EvictArgs a{};
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.keep_lens = keep_lens;
+  a.mass_in = in->mass;
+  a.positions_in = in->positions;
+  a.history_in = in->history;
+  a.mass_out = out->mass;
+  a.positions_out = out->positions;
+  a.history_out = out->history;
+  a.in_stride = in->stride;
+  a.out_stride = out->stride;
+  a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + w.counts);
+  a.moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) + w.moves);
+  a.err = dev->err;
+  a.num_blocks = pool->num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.max_context_len = maxL;
+  a.move_cap = (int32_t)w.cap;
+  a.sinks = sinks;
+  a.recent = recent;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  evict_select_kernel<<<num_seqs, 1024, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "evict select launch");
+  // the number of moves is known on the device only: enough CTAs to fill the GPU
+  const int64_t chunks = w.cap * block_bytes(pool) / kBlock / (is_q4(pool) ? 4 : 16);
+  const int64_t want = std::max<int64_t>(1, (int64_t)dev->num_sms * 8 / num_seqs);
+  const dim3 grid((unsigned)std::min<int64_t>((chunks + 255) / 256, want), (unsigned)num_seqs);
+  if (is_q4(pool))
+    evict_move_q4_kernel<<<grid, 256, 0, s>>>(a, static_cast<uint8_t*>(k_pool),
+                                              static_cast<uint8_t*>(v_pool), pool->heads, pool->head_dim);
+  else
+    evict_move_kernel<<<grid, 256, 0, s>>>(a, static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool),
+                                           pool->heads, pool->head_dim * pool->elem_bytes / 16);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "evict move launch");
 }
 
 pa_status pa_selftest_wait_timeout(void* stream) {

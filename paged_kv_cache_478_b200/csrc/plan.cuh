@@ -73,6 +73,10 @@ struct DecodeArgs {
   float scale_log2;  // scale * log2(e)
   uint64_t stamp;    // number of the plan the host expects in the workspace
   int32_t after_plan;  // launched as a programmatic dependent of the plan kernel: wait for it first
+  // weight gathering (mass.cuh), null otherwise
+  float* scores;         // [S][query heads][score_stride] scaled scores in log2 units
+  float* lse;            // [S][query heads] log2 of the softmax sum
+  int64_t score_stride;  // tokens between query heads of scores
 };
 
 // Checks a CTA makes before it trusts the plan in the workspace: the header

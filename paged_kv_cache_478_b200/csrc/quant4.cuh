@@ -1,0 +1,265 @@
+// The 4-bit pool: its format, and the kernels that write and convert it.
+//
+// Each (block, head) tile of a 4-bit K or V pool is 9 * D bytes:
+//   [0, 8 D)    data [D / 32 pieces][16 tokens][16 bytes]: byte b of piece c
+//               holds dimension 32 c + 2 b in its low half, 32 c + 2 b + 1 in
+//               its high half;
+//   [8 D, 9 D)  one 32-bit word per group of 64 dimensions, [D / 64][16
+//               tokens]: the group's scale s (bf16) in the upper half, its
+//               zero point z (a whole number, fp16) in the lower.
+// A held number n stands for s * (n - z): 4.5 bits a value.  The 16-byte
+// pieces of 8 consecutive tokens are 128 contiguous bytes, so that the matrix
+// loads (ldmatrix) of the attention kernel are free of bank conflicts.
+//
+// Quantisation of a group of 64 values x, in fp32:
+//   s = bf16(max((max x - min x) / 15, max |x| / 2000)),  z = round(-min x / s),
+//   n = clamp(round(x / s) + z, 0, 15)       (n = z = 0 where s = 0).
+// z may lie outside 0..15, so a group far from zero keeps the full
+// resolution of its range; the second term of s keeps |z| below 2048, where
+// fp16 holds every whole number.  The error is at most s / 2, and a few
+// hundredths of s more at the upper end where s was rounded down.  x / s has
+// a quotient of at most 11 by 8 significant bits, which is never so near to a
+// half without being one that fp32 division would round it there: n and z are
+// those of exact arithmetic.  A group that holds an infinity or NaN, or whose
+// range passes fp32, gets s = NaN and reads back as NaN.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "device_utils.cuh"
+#include "pagedattn.h"
+#include "plan.cuh"
+
+namespace pa {
+
+// Bytes of one (block, head) tile, and the offset of its words.
+__host__ __device__ constexpr int q4_tile_bytes(int D) { return 9 * D; }
+__host__ __device__ constexpr int q4_words_off(int D) { return 8 * D; }
+
+__device__ __forceinline__ float q4_scale(uint32_t word) { return __uint_as_float(word & 0xffff0000u); }
+__device__ __forceinline__ float q4_zero(uint32_t word) {
+  return __half2float(__ushort_as_half((unsigned short)(word & 0xffffu)));
+}
+
+// Quantise one group of 64 values held by 8 neighbouring lanes, 8 each (all
+// 32 lanes of the warp call).  Returns the lane's 8 numbers, the first in the
+// lowest 4 bits; *word is the group's word.
+__device__ __forceinline__ uint32_t q4_quantise(const float* x, int lane, uint32_t* word) {
+  float hi = x[0], lo = x[0], probe = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi = fmaxf(hi, x[e]);
+    lo = fminf(lo, x[e]);
+    probe = fmaf(x[e], 0.f, probe);  // NaN once any value is an infinity or NaN
+  }
+  const uint32_t bad = __ballot_sync(kFullMask, probe != 0.f);
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, m));
+    lo = fminf(lo, __shfl_xor_sync(kFullMask, lo, m));
+  }
+  const float range = __fsub_rn(hi, lo);
+  const float top = fmaxf(fabsf(hi), fabsf(lo));
+  const float raw = fmaxf(__fdiv_rn(range, 15.f), __fdiv_rn(top, 2000.f));
+  const float s = __bfloat162float(__float2bfloat16_rn(raw));
+  if (((bad >> (lane & 24)) & 0xffu) != 0u || !(s < INFINITY)) {
+    *word = 0x7fc00000u;  // s = NaN, z = 0
+    return 0u;
+  }
+  if (s == 0.f) {
+    *word = 0u;
+    return 0u;
+  }
+  const float z = rintf(__fdiv_rn(-lo, s));
+  uint32_t n = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + z, 0.f), 15.f);
+    n |= (uint32_t)v << (4 * e);
+  }
+  *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
+  return n;
+}
+
+// Where the lane's 8 numbers of (row t, group g) go in a tile: lane j of the
+// 8 holds dimensions 64 g + 8 j .. + 7.
+__device__ __forceinline__ int q4_data_off(int g, int j, int t) {
+  return (2 * g + (j >> 2)) * 256 + t * 16 + (j & 3) * 4;
+}
+
+// Append: each new token's K and V rows are quantised into the slot that
+// slot_mapping names.  Eight lanes take one (token, head, group of 64): one
+// 16-byte load of K and of V per lane, one 4-byte store each.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    q4_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new,
+                     const int32_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_pool,
+                     uint8_t* __restrict__ v_pool, int heads, int D, int64_t num_tokens,
+                     int64_t num_slots, uint32_t* err) {
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  const int groups = D / 64;
+  const int64_t total = num_tokens * heads * groups;
+  // every lane of a warp runs the same number of rounds (the shuffles need all of them)
+  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
+       w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+    const int64_t u = w * 4 + (lane >> 3);
+    const bool live = u < total;
+    const int64_t row = live ? u / groups : 0;  // token * heads + head
+    const int g = live ? (int)(u - row * groups) : 0;
+    const int64_t t = row / heads;
+    const int h = (int)(row - t * heads);
+    const int32_t slot = live ? slot_mapping[t] : -1;
+    if (slot >= num_slots && h == 0 && g == 0 && j == 0) atomicOr(err, PA_DEVERR_SLOT);
+    const bool write = slot >= 0 && slot < num_slots;  // a negative slot is padding
+    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+    if (write) {
+      const int64_t src = row * D + g * 64 + j * 8;
+      ku = *reinterpret_cast<const uint4*>(k_new + src);
+      vu = *reinterpret_cast<const uint4*>(v_new + src);
+    }
+    float kf[8], vf[8];
+    Chunk<T>::to_float(ku, kf);
+    Chunk<T>::to_float(vu, vf);
+    uint32_t kw, vw;
+    const uint32_t kn = q4_quantise(kf, lane, &kw);
+    const uint32_t vn = q4_quantise(vf, lane, &vw);
+    if (write) {
+      const int64_t tile = ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D);
+      const int r = slot & 15;
+      *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g, j, r)) = kn;
+      *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g, j, r)) = vn;
+      if (j == 0) {
+        *reinterpret_cast<uint32_t*>(k_pool + tile + q4_words_off(D) + (g * 16 + r) * 4) = kw;
+        *reinterpret_cast<uint32_t*>(v_pool + tile + q4_words_off(D) + (g * 16 + r) * 4) = vw;
+      }
+    }
+  }
+}
+
+// The same for each sequence's new token, k_new and v_new [S][heads][D], at the
+// last position of its planned length (the fused append's contract).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    q4_append_last_kernel(DecodeArgs a, const T* __restrict__ k_new, const T* __restrict__ v_new, int D) {
+  if (!plan_header_ok(a)) return;  // the decode launch that follows reports it
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  const int groups = D / 64;
+  const int64_t total = (int64_t)a.num_seqs * a.heads * groups;
+  const int64_t cap = min((int64_t)a.max_context_len, (int64_t)a.max_blocks_per_seq * kBlock);
+  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
+       w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+    const int64_t u = w * 4 + (lane >> 3);
+    const bool live = u < total;
+    const int64_t row = live ? u / groups : 0;  // sequence * heads + head
+    const int g = live ? (int)(u - row * groups) : 0;
+    const int s = (int)(row / a.heads);
+    const int h = (int)(row - (int64_t)s * a.heads);
+    const int L = live ? a.lens[s] : 0;
+    bool write = L > 0 && L <= cap;
+    int32_t b = 0;
+    if (write) {
+      b = a.block_tables[(int64_t)s * a.max_blocks_per_seq + (L - 1) / kBlock];
+      write = b >= 0 && b < a.num_blocks;  // the decode launch reports a bad one
+    }
+    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+    if (write) {
+      const int64_t src = row * D + g * 64 + j * 8;
+      ku = *reinterpret_cast<const uint4*>(k_new + src);
+      vu = *reinterpret_cast<const uint4*>(v_new + src);
+    }
+    float kf[8], vf[8];
+    Chunk<T>::to_float(ku, kf);
+    Chunk<T>::to_float(vu, vf);
+    uint32_t kw, vw;
+    const uint32_t kn = q4_quantise(kf, lane, &kw);
+    const uint32_t vn = q4_quantise(vf, lane, &vw);
+    if (write) {
+      const int64_t tile = ((int64_t)b * a.heads + h) * q4_tile_bytes(D);
+      const int r = (L - 1) % kBlock;
+      uint8_t* kt = static_cast<uint8_t*>(const_cast<void*>(a.k_pool)) + tile;
+      uint8_t* vt = static_cast<uint8_t*>(const_cast<void*>(a.v_pool)) + tile;
+      *reinterpret_cast<uint32_t*>(kt + q4_data_off(g, j, r)) = kn;
+      *reinterpret_cast<uint32_t*>(vt + q4_data_off(g, j, r)) = vn;
+      if (j == 0) {
+        *reinterpret_cast<uint32_t*>(kt + q4_words_off(D) + (g * 16 + r) * 4) = kw;
+        *reinterpret_cast<uint32_t*>(vt + q4_words_off(D) + (g * 16 + r) * 4) = vw;
+      }
+    }
+  }
+}
+
+// Whole blocks from a 16-bit pool into a 4-bit one (PACK) or back, for every
+// (src, dst) pair.  Eight lanes take one (pair, head, group, token); tokens
+// are innermost, so the stores of a warp's four tokens are contiguous.
+template <typename T, bool PACK>
+__global__ void __launch_bounds__(256)
+    q4_convert_kernel(const uint8_t* __restrict__ k_src, const uint8_t* __restrict__ v_src,
+                      uint8_t* __restrict__ k_dst, uint8_t* __restrict__ v_dst,
+                      const int32_t* __restrict__ pairs, int64_t num_pairs, int64_t src_blocks,
+                      int64_t dst_blocks, int heads, int D, uint32_t* err) {
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  const int groups = D / 64;
+  const int64_t total = num_pairs * heads * groups * kBlock;  // a multiple of 4
+  const int64_t wide = (int64_t)kBlock * D * sizeof(T);
+  const int narrow = q4_tile_bytes(D);
+  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
+       w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+    const int64_t u = w * 4 + (lane >> 3);
+    const int t = (int)(u % kBlock);
+    int64_t rest = u / kBlock;
+    const int g = (int)(rest % groups);
+    rest /= groups;
+    const int h = (int)(rest % heads);
+    const int64_t p = rest / heads;
+    const int32_t src = pairs[2 * p], dst = pairs[2 * p + 1];
+    if (src < 0 || src >= src_blocks || dst < 0 || dst >= dst_blocks) {  // the same for the warp
+      if (h == 0 && g == 0 && t == 0 && j == 0) atomicOr(err, PA_DEVERR_PAIR);
+      continue;
+    }
+    const int64_t row16 = (int64_t)t * D * sizeof(T) + (g * 64 + j * 8) * sizeof(T);
+    if constexpr (PACK) {
+      const int64_t from = ((int64_t)src * heads + h) * wide + row16;
+      const uint4 ku = *reinterpret_cast<const uint4*>(k_src + from);
+      const uint4 vu = *reinterpret_cast<const uint4*>(v_src + from);
+      float kf[8], vf[8];
+      Chunk<T>::to_float(ku, kf);
+      Chunk<T>::to_float(vu, vf);
+      uint32_t kw, vw;
+      const uint32_t kn = q4_quantise(kf, lane, &kw);
+      const uint32_t vn = q4_quantise(vf, lane, &vw);
+      const int64_t tile = ((int64_t)dst * heads + h) * narrow;
+      *reinterpret_cast<uint32_t*>(k_dst + tile + q4_data_off(g, j, t)) = kn;
+      *reinterpret_cast<uint32_t*>(v_dst + tile + q4_data_off(g, j, t)) = vn;
+      if (j == 0) {
+        *reinterpret_cast<uint32_t*>(k_dst + tile + q4_words_off(D) + (g * 16 + t) * 4) = kw;
+        *reinterpret_cast<uint32_t*>(v_dst + tile + q4_words_off(D) + (g * 16 + t) * 4) = vw;
+      }
+    } else {
+      const int64_t tile = ((int64_t)src * heads + h) * narrow;
+      const int64_t to = ((int64_t)dst * heads + h) * wide + row16;
+      // the largest finite value of T: the last step of a group may pass it
+      constexpr float kTop = std::is_same<T, __half>::value ? 65504.f : 3.38953139e38f;
+      auto one = [&](const uint8_t* from, uint8_t* into) {
+        const uint32_t n = *reinterpret_cast<const uint32_t*>(from + tile + q4_data_off(g, j, t));
+        const uint32_t word =
+            *reinterpret_cast<const uint32_t*>(from + tile + q4_words_off(D) + (g * 16 + t) * 4);
+        const float s = q4_scale(word), z = q4_zero(word);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // exact in fp32 (8 by 12 bits), rounded once to T below
+          const float v = s * ((float)((n >> (4 * e)) & 15u) - z);
+          f[e] = v > kTop ? kTop : v < -kTop ? -kTop : v;  // NaN stays
+        }
+        *reinterpret_cast<uint4*>(into + to) = Chunk<T>::from_float(f);
+      };
+      one(k_src, k_dst);
+      one(v_src, v_dst);
+    }
+  }
+}
+
+}  // namespace pa

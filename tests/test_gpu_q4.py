@@ -1,0 +1,398 @@
+"""4-bit pools on the GPU against the fp64 oracle: append, conversion, copies
+(bit for bit) and decode attention (element by element).
+
+Tolerance of the attention, from the arithmetic (D dimensions, N tokens):
+  out = sum_t w_t v_t.  The output is rounded once (half a step, eps / 2).  Each
+  numerator weight, times its scale, is rounded once to fp16: 2^-11 of it, or
+  2^-25 of the largest where it is subnormal.  A score is an fp32 sum of D products
+  and of the zero point's term, off by at most D 2^-24 scale sum |q| s (n + |z|) =: e;
+  with the exponential's own 2^-22 that moves a weight by a factor of 1 + e + 2^-22,
+  in the numerator and in the denominator.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_478_b200 as pa
+from oracle import compress as oc
+from paged_kv_cache_478_b200 import synthetic as syn
+from tests.gpu_cases import workspace_for
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": (torch.float16, pa.PA_Q4_F16), "bf16": (torch.bfloat16, pa.PA_Q4_BF16)}
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    if torch.cuda.is_available():
+        pa.pa_device_errors()
+    yield
+
+
+def as_type(x, kind):
+    """numpy -> (CUDA tensor of the type, its exact values as float64)."""
+    t = torch.from_numpy(np.ascontiguousarray(x)).to(TYPES[kind][0])
+    return t.cuda(), t.double().numpy()
+
+
+def random_rows(rng, n, heads, dim):
+    """Rows whose channels differ in size and offset, with a few outliers."""
+    size = np.exp(rng.standard_normal(dim))
+    x = rng.standard_normal((n, heads, dim)) * size + 0.5 * size[::-1]
+    x[rng.random(x.shape) < 0.01] *= 10
+    return x
+
+
+def filled_pool(rng, nb, heads, dim, kind, fill=0xFF):
+    """A pool of quantised random rows, host bytes (fill: other bytes, 0xFF is a NaN scale)."""
+    pool = np.full((nb, heads, 9 * dim), fill, dtype=np.uint8)
+    _, x = as_type(random_rows(rng, nb * 16, heads, dim), kind)
+    for r in range(nb * 16):
+        for h in range(heads):
+            oc.store_row(pool, r // 16, h, r % 16, x[r, h])
+    return pool
+
+
+def cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+# ---- append ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,tokens", [(1, 1), (3, 5), (2, 33), (5, 16)])
+def test_append_is_bit_exact(kind, dim, heads, tokens):
+    rng = np.random.default_rng(tokens * 10 + heads)
+    nb = 4
+    kn, kx = as_type(random_rows(rng, tokens, heads, dim), kind)
+    vn, vx = as_type(random_rows(rng, tokens, heads, dim), kind)
+    slots = rng.permutation(nb * 16)[:tokens].astype(np.int32)
+    if tokens > 2:
+        slots[1] = -1  # padding
+    kp = rng.integers(0, 256, (nb, heads, 9 * dim)).astype(np.uint8)
+    vp = rng.integers(0, 256, (nb, heads, 9 * dim)).astype(np.uint8)
+    kd, vd = cuda(kp), cuda(vp)
+    pool = pa.pa_pool_create(nb, 16, heads, dim, TYPES[kind][1])
+    pa.pa_reshape_and_cache(pool, kn, vn, cuda(slots), kd, vd)
+    assert pa.pa_device_errors() == 0
+    for t in range(tokens):
+        for h in range(heads if slots[t] >= 0 else 0):
+            oc.store_row(kp, slots[t] // 16, h, slots[t] % 16, kx[t, h])
+            oc.store_row(vp, slots[t] // 16, h, slots[t] % 16, vx[t, h])
+    assert np.array_equal(kd.cpu().numpy(), kp) and np.array_equal(vd.cpu().numpy(), vp)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_append_of_special_rows(kind):
+    """Zeros, constants, far offsets, the type's extremes, subnormals, infinities and NaN."""
+    dim, top = 64, float(torch.finfo(TYPES[kind][0]).max)
+    tiny = float(torch.finfo(TYPES[kind][0]).smallest_normal) / 8
+    rng = np.random.default_rng(3)
+    rows = [np.zeros(dim), np.full(dim, 5.0), np.full(dim, -7.25), 1000 + rng.standard_normal(dim),
+            np.where(np.arange(dim) % 2, 1.0, -1.0), rng.standard_normal(dim) * tiny,
+            np.r_[np.zeros(dim - 1), tiny], np.r_[top, rng.standard_normal(dim - 1)],
+            np.r_[np.nan, np.ones(dim - 1)], np.r_[np.ones(dim - 1), np.inf],
+            np.r_[-np.inf, np.inf, np.zeros(dim - 2)], np.r_[top, -top, np.zeros(dim - 2)],
+            np.arange(dim) / 4.0, -np.arange(dim) / 8.0, np.r_[0.5, 15.5, np.arange(dim - 2) % 16]]
+    x = np.stack(rows)[:, None]
+    kn, kx = as_type(x, kind)
+    pool = pa.pa_pool_create(1, 16, 1, dim, TYPES[kind][1])
+    kd, vd = torch.zeros((1, 1, 9 * dim), dtype=torch.uint8, device="cuda"), torch.zeros((1, 1, 9 * dim), dtype=torch.uint8, device="cuda")
+    pa.pa_reshape_and_cache(pool, kn, kn, torch.arange(len(rows), dtype=torch.int32, device="cuda"), kd, vd)
+    want = np.zeros((1, 1, 9 * dim), dtype=np.uint8)
+    for r in range(len(rows)):
+        oc.store_row(want, 0, 0, r, kx[r, 0])
+    got = oc.values(kd.cpu().numpy(), dim)[0, 0, :len(rows)]
+    ref = oc.values(want, dim)[0, 0, :len(rows)]
+    assert np.array_equal(got, ref, equal_nan=True)
+    assert torch.equal(kd, vd)
+
+
+def test_append_reports_bad_slots_and_writes_nothing_there():
+    pool = pa.pa_pool_create(2, 16, 3, 64, pa.PA_Q4_F16)
+    k = torch.zeros((2, 3, 576), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    new = torch.ones((2, 3, 64), dtype=torch.float16, device="cuda")
+    pa.pa_reshape_and_cache(pool, new, new, torch.tensor([32, -5], dtype=torch.int32, device="cuda"), k, v)
+    assert pa.pa_device_errors() == pa.PA_DEVERR_SLOT
+    assert not k.any() and not v.any()
+
+
+# ---- conversion and copies ---------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim,heads", [(64, 1), (64, 3), (128, 5)])
+def test_convert_blocks_both_ways(kind, dim, heads):
+    rng = np.random.default_rng(dim + heads)
+    nb = 7
+    x16, x = as_type(random_rows(rng, nb * 16, heads, dim).reshape(nb, 16, heads, dim).transpose(0, 2, 1, 3), kind)
+    y16, y = as_type(random_rows(rng, nb * 16, heads, dim).reshape(nb, 16, heads, dim).transpose(0, 2, 1, 3), kind)
+    wide = pa.pa_pool_create(nb, 16, heads, dim, TYPES[kind][0])
+    four = pa.pa_pool_create(nb + 2, 16, heads, dim, TYPES[kind][1])
+    k4 = torch.zeros((nb + 2, heads, 9 * dim), dtype=torch.uint8, device="cuda")
+    v4 = torch.zeros_like(k4)
+    pairs = np.array([[0, 8], [6, 1], [2, 2], [3, 0]], dtype=np.int32)
+    pa.pa_convert_blocks(wide, x16, y16, four, k4, v4, cuda(pairs))
+    assert pa.pa_device_errors() == 0
+    want_k, want_v = np.zeros(k4.shape, dtype=np.uint8), np.zeros(k4.shape, dtype=np.uint8)
+    for a, b in pairs:
+        for h in range(heads):
+            for t in range(16):
+                oc.store_row(want_k, b, h, t, x[a, h, t])
+                oc.store_row(want_v, b, h, t, y[a, h, t])
+    assert np.array_equal(k4.cpu().numpy(), want_k) and np.array_equal(v4.cpu().numpy(), want_v)
+    back_k, back_v = torch.full_like(x16, 3.0), torch.full_like(x16, 3.0)
+    back = np.array([[8, 5], [1, 4], [0, 6]], dtype=np.int32)
+    pa.pa_convert_blocks(four, k4, v4, wide, back_k, back_v, cuda(back))
+    assert pa.pa_device_errors() == 0
+    for got, pool in ((back_k, want_k), (back_v, want_v)):
+        ref = torch.full((nb, heads, 16, dim), 3.0, dtype=torch.float64)
+        vals = torch.from_numpy(oc.values(pool, dim))
+        for a, b in back:
+            ref[b] = vals[a]
+        assert torch.equal(got.cpu(), ref.to(TYPES[kind][0]))
+
+
+def test_convert_holds_the_finite_range():
+    """fp16: the last step of a group near the type's largest value may pass it."""
+    dim = 64
+    x = np.zeros((1, 1, 16, dim))
+    x[0, 0, :, 0] = 65504.0
+    x[0, 0, :, 1] = -np.linspace(1, 65504, 16)
+    x16, _ = as_type(x, "f16")
+    wide, four = pa.pa_pool_create(1, 16, 1, dim, torch.float16), pa.pa_pool_create(1, 16, 1, dim, pa.PA_Q4_F16)
+    k4, v4 = torch.zeros((1, 1, 576), dtype=torch.uint8, device="cuda"), torch.zeros((1, 1, 576), dtype=torch.uint8, device="cuda")
+    pairs = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    pa.pa_convert_blocks(wide, x16, x16, four, k4, v4, pairs)
+    out = torch.zeros_like(x16)
+    pa.pa_convert_blocks(four, k4, v4, wide, out, torch.zeros_like(out), pairs)
+    ref = np.clip(oc.values(k4.cpu().numpy(), dim), -65504, 65504)
+    assert np.abs(oc.values(k4.cpu().numpy(), dim)).max() > 65504  # the clamp is reached
+    assert np.array_equal(out.cpu().double().numpy(), ref.astype(np.float16).astype(np.float64))
+
+
+def test_convert_and_copy_report_bad_pairs():
+    wide, four = pa.pa_pool_create(3, 16, 2, 64, torch.float16), pa.pa_pool_create(5, 16, 2, 64, pa.PA_Q4_F16)
+    x = torch.ones((3, 2, 16, 64), dtype=torch.float16, device="cuda")
+    k, v = torch.zeros((5, 2, 576), dtype=torch.uint8, device="cuda"), torch.zeros((5, 2, 576), dtype=torch.uint8, device="cuda")
+    bad = torch.tensor([[3, 0], [-1, 1], [0, 5], [0, -2], [1, 4]], dtype=torch.int32, device="cuda")
+    pa.pa_convert_blocks(wide, x, x, four, k, v, bad)
+    assert pa.pa_device_errors() == pa.PA_DEVERR_PAIR
+    assert not k[:4].any() and k[4].any()
+    pa.pa_copy_blocks(four, k, v, torch.tensor([[4, 0], [5, 1]], dtype=torch.int32, device="cuda"))
+    assert pa.pa_device_errors() == pa.PA_DEVERR_PAIR
+    assert torch.equal(k[0], k[4]) and torch.equal(v[0], v[4]) and not k[1:4].any()
+
+
+# ---- decode -------------------------------------------------------------------------------
+
+EDGE_LENGTHS = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 256, 257, 600]
+
+
+def decode_case(seed, lengths, heads, group, dim, kind, spread=random_rows, shared_rows=None):
+    """A decode problem over quantised pools; every byte outside the cached tokens is 0xFF
+    (NaN scales), so that anything read there shows."""
+    rng = np.random.default_rng(seed)
+    need = [-(-n // 16) for n in lengths]
+    nb, wide = sum(need) + 1, max(need + [1])
+    tables = syn.random_tables(rng, lengths, nb, wide)
+    kp = np.full((nb, heads, 9 * dim), 0xFF, dtype=np.uint8)
+    vp = kp.copy()
+    rows = sum(lengths)
+    _, kx = as_type(spread(rng, rows, heads, dim), kind)
+    _, vx = as_type(spread(rng, rows, heads, dim), kind)
+    r = 0
+    for s, n in enumerate(lengths):
+        for t in range(n):
+            for h in range(heads):
+                oc.store_row(kp, tables[s, t // 16], h, t % 16, kx[r, h])
+                oc.store_row(vp, tables[s, t // 16], h, t % 16, vx[r, h])
+            r += 1
+    q, qx = as_type(rng.standard_normal((len(lengths), heads * group, dim)), kind)
+    return dict(kp=kp, vp=vp, tables=tables, lens=np.array(lengths, dtype=np.int32), q=q, qx=qx, heads=heads, group=group,
+                dim=dim, kind=kind, scale=1 / math.sqrt(dim))
+
+
+def run_decode(c, partition=0, **kw):
+    nb = c["kp"].shape[0]
+    pool = pa.pa_pool_create(nb, 16, c["heads"], c["dim"], TYPES[c["kind"]][1])
+    pa.pa_pool_set_query_heads(pool, c["heads"] * c["group"])
+    out = torch.full_like(c["q"], float("nan"))
+    ws = workspace_for(pool, len(c["lens"]), c["tables"].shape[1], 0, partition)
+    pa.pa_decode_attention(pool, c["q"], cuda(c["kp"]), cuda(c["vp"]), cuda(c["tables"]), cuda(c["lens"]), c["scale"], out, ws,
+                           partition_size=partition, **kw)
+    return out
+
+
+def reference(c):
+    n, s, z = oc.parts(c["kp"], c["dim"])
+    k, v = oc.values(c["kp"], c["dim"]), oc.values(c["vp"], c["dim"])
+    out, weights, bound = oc.attend(c["qx"], k, v, c["lens"], c["tables"], c["scale"])
+    eps = torch.finfo(TYPES[c["kind"]][0]).eps
+    tol = np.zeros_like(out)
+    mag = np.repeat(s, 64, -1) * (n + np.abs(np.repeat(z, 64, -1)))
+    for i, L in enumerate(c["lens"]):
+        for h in range(out.shape[1] if L else 0):
+            hk = h // c["group"]
+            rows = np.stack([mag[c["tables"][i, t // 16], hk, t % 16] for t in range(L)])
+            vals = np.stack([v[c["tables"][i, t // 16], hk, t % 16] for t in range(L)])
+            e = c["dim"] * 2.0 ** -24 * c["scale"] * (rows @ np.abs(c["qx"][i, h])).max() + 2.0 ** -22
+            tol[i, h] = (eps / 2 * np.abs(out[i, h]) * 1.01 + (1.01 * 2.0 ** -11 + 2 * e) * bound[i, h]
+                         + L * 2.0 ** -25 * np.abs(vals).max() + torch.finfo(TYPES[c["kind"]][0]).smallest_normal * eps)
+    return out, tol, weights
+
+
+def check(got, want, tol):
+    g = got.double().cpu().numpy()
+    bad = ~(np.abs(g - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), float(np.nanmax(np.abs(g - want) / np.maximum(tol, 1e-30))))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group", [(1, 1), (2, 4), (3, 2), (6, 1), (1, 8), (4, 8)])
+def test_decode_lengths_and_heads(kind, dim, heads, group):
+    lengths = EDGE_LENGTHS if heads * group <= 8 else [0, 1, 17, 64, 130, 257]
+    c = decode_case(heads * 100 + group, lengths, heads, group, dim, kind)
+    want, tol, _ = reference(c)
+    for partition in (0, 16, 64, 208):
+        check(run_decode(c, partition), want, tol)
+        assert pa.pa_device_errors() == 0
+
+
+def offset_rows(rng, n, heads, dim):
+    return 50 + rng.standard_normal((n, heads, dim))
+
+
+def sized_rows(rng, n, heads, dim):
+    """Tokens whose sizes differ by many powers of two."""
+    return rng.standard_normal((n, heads, dim)) * 2.0 ** rng.integers(-12, 3, (n, 1, 1))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("spread", [offset_rows, sized_rows])
+def test_decode_of_uneven_values(kind, spread):
+    c = decode_case(5, [200, 77, 16], 2, 4, 128, kind, spread)
+    want, tol, _ = reference(c)
+    for partition in (0, 64):
+        check(run_decode(c, partition), want, tol)
+
+
+def test_decode_of_large_and_small_bf16_values():
+    """Values far outside fp16's range, in a type that holds them."""
+    for size in (1e30, 1e-30):
+        c = decode_case(6, [100, 3], 1, 2, 64, "bf16", lambda rng, n, h, d: size * rng.standard_normal((n, h, d)))
+        c["q"], c["qx"] = as_type(c["qx"] / size, "bf16")
+        want, tol, _ = reference(c)
+        check(run_decode(c), want, tol)
+
+
+def test_nan_values_reach_their_own_group_only():
+    c = decode_case(7, [40], 1, 1, 128, "f16")
+    row = oc.values(c["vp"], 128)[c["tables"][0, 1], 0, 3].copy()
+    row[100] = np.nan
+    oc.store_row(c["vp"], c["tables"][0, 1], 0, 3, row)
+    got = run_decode(c)[0, 0]
+    assert torch.isnan(got[64:]).all() and torch.isfinite(got[:64]).all()
+
+
+def test_bad_block_ids_are_reported():
+    c = decode_case(8, [40, 20], 2, 1, 64, "f16")
+    c["tables"][0, 1] = 10 ** 6
+    c["tables"][1, 0] = -3
+    run_decode(c)
+    assert pa.pa_device_errors() == pa.PA_DEVERR_BLOCK_ID
+
+
+def test_results_repeat_bit_for_bit_and_do_not_depend_on_placement():
+    c = decode_case(9, [300, 50], 2, 2, 128, "bf16")
+    a = run_decode(c, 64)
+    assert torch.equal(a, run_decode(c, 64))
+    nb = c["kp"].shape[0]
+    perm = np.random.default_rng(1).permutation(nb)
+    moved = dict(c, kp=c["kp"][np.argsort(perm)], vp=c["vp"][np.argsort(perm)],
+                 tables=np.where(c["tables"] >= 0, perm[c["tables"]], -1).astype(np.int32))
+    assert torch.equal(a, run_decode(moved, 64))
+
+
+@pytest.mark.parametrize("group", [1, 4])
+def test_append_and_attend_planned_in_a_graph(group):
+    """The serving step: plan once, then append + attend, captured on a side stream and
+    replayed; the same as the separate calls, pools included."""
+    lengths = [1, 16, 17, 0, 140]
+    c = decode_case(10, lengths, 3, group, 128, "f16")
+    S, heads, dim = len(lengths), 3, 128
+    rng = np.random.default_rng(4)
+    kn, vn = as_type(random_rows(rng, S, heads, dim), "f16")[0], as_type(random_rows(rng, S, heads, dim), "f16")[0]
+    nb = c["kp"].shape[0]
+    pool = pa.pa_pool_create(nb, 16, heads, dim, pa.PA_Q4_F16)
+    pa.pa_pool_set_query_heads(pool, heads * group)
+    bt, cl = cuda(c["tables"]), cuda(c["lens"])
+    k1, v1, k2, v2 = (cuda(x) for x in (c["kp"], c["vp"], c["kp"], c["vp"]))
+    ws1, ws2 = (workspace_for(pool, S, bt.shape[1], 0, 64) for _ in range(2))
+    slots = cuda(pa.pa_decode_slots(c["tables"], c["lens"]))
+    want, got, once = (torch.full_like(c["q"], float("nan")) for _ in range(3))
+    pa.pa_reshape_and_cache(pool, kn, vn, slots, k1, v1)
+    pa.pa_decode_attention(pool, c["q"], k1, v1, bt, cl, c["scale"], want, ws1, partition_size=64)
+    k3, v3 = cuda(c["kp"]), cuda(c["vp"])
+    pa.pa_decode_append_attention(pool, c["q"], kn, vn, k3, v3, bt, cl, c["scale"], once, ws1, partition_size=64)
+    assert torch.equal(once, want) and torch.equal(k3, k1) and torch.equal(v3, v1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pa.pa_decode_plan(pool, cl, bt.shape[1], ws2, partition_size=64)
+        pa.pa_decode_append_attention_planned(pool, c["q"], kn, vn, k2, v2, bt, c["scale"], got, ws2, partition_size=64)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(k2, k1) and torch.equal(v2, v1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        pa.pa_decode_append_attention_planned(pool, c["q"], kn, vn, k2, v2, bt, c["scale"], got, ws2, partition_size=64)
+    for _ in range(3):
+        got.fill_(float("nan"))
+        k2.copy_(cuda(c["kp"]))
+        v2.copy_(cuda(c["vp"]))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(k2, k1) and torch.equal(v2, v1)
+    assert pa.pa_device_errors() == 0
+
+
+def test_planned_calls_refuse_a_plan_of_another_pool_type():
+    c = decode_case(11, [20], 4, 1, 64, "f16")
+    nb = c["kp"].shape[0]
+    wide, four = pa.pa_pool_create(nb, 16, 4, 64, torch.float16), pa.pa_pool_create(nb, 16, 4, 64, pa.PA_Q4_F16)
+    ws = workspace_for(four, 1, c["tables"].shape[1])
+    pa.pa_decode_plan(wide, cuda(c["lens"]), c["tables"].shape[1], ws)
+    with pytest.raises(pa.PagedAttnError) as e:
+        pa.pa_decode_attention_planned(four, c["q"], cuda(c["kp"]), cuda(c["vp"]), cuda(c["tables"]), c["scale"],
+                                       torch.empty_like(c["q"]), ws)
+    assert e.value.status == 1
+
+
+def test_static_scratch():
+    c = decode_case(12, [100, 31], 2, 2, 64, "bf16")
+    nb = c["kp"].shape[0]
+    pool = pa.pa_pool_create(nb, 16, 2, 64, pa.PA_Q4_BF16)
+    pa.pa_pool_set_query_heads(pool, 4)
+    out = torch.empty_like(c["q"])
+    pa.pa_decode_attention_static(pool, c["q"], cuda(c["kp"]), cuda(c["vp"]), cuda(c["tables"]), cuda(c["lens"]), c["scale"], out,
+                                  partition_size=64)
+    assert torch.equal(out, run_decode(c, 64))
+
+
+def test_wrong_tensors_are_refused_by_the_binding():
+    pool = pa.pa_pool_create(2, 16, 2, 64, pa.PA_Q4_F16)
+    k = torch.zeros((2, 2, 576), dtype=torch.uint8, device="cuda")
+    new = torch.ones((1, 2, 64), dtype=torch.float16, device="cuda")
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        pa.pa_reshape_and_cache(pool, new, new, slot, k[:1], k)
+    with pytest.raises(TypeError):
+        pa.pa_reshape_and_cache(pool, new, new, slot, k.view(torch.int8), k)
+    with pytest.raises(TypeError):
+        pa.pa_reshape_and_cache(pool, new.bfloat16(), new, slot, k, k)
