@@ -1,53 +1,132 @@
 // Decode attention over 4-bit pools (quant4.cuh has the format).
 //
 // Work items, plan, split-K partials and merge are those of the other decode
-// kernels (plan.cuh, decode.cuh).  One warp owns one KV head of the item and
-// all of its G query heads.
+// kernels (plan.cuh, decode.cuh).  A warp streams the K and V tiles of one KV
+// head through its own ring of bulk copies, 64 tokens (4 blocks) a stage, and
+// serves all G query heads of it.
+//
+// The products run on the tensor cores without an integer conversion of the
+// held numbers: 4 bits n in the low bits of an fp16 word ARE the number n 2^-24
+// (a subnormal), and bits 4-7 are n 2^-20, so one AND and one fp16 FMA make (n - z)
+// 2^-10 of two numbers, exactly (|n - z| is below 2048).  Feeding the subnormals
+// themselves to the matrix instructions would save the FMA, but those line up a
+// sum by the exponents its operands are written with: subnormals cost it 6 to 10
+// bits (measured: sums off by 2^-18 of their terms).
+//   scores:  x_t = sum_g s_t,g sum_d q_d (n_t,d - z_t,g), g a group of 64 dimensions.
+//     Q is the A operand (16 rows, G of them used), scaled by a power of two
+//     into fp16's range (exact for fp16 and bf16 queries).
+//   values:  o_d = sum_t P_t,g (n_t,d - z_t,g),  P_t,g = w_t s_t,g.
+//     V^T is the A operand, P the B operand: the layout in which the scores'
+//     accumulators leave the tensor cores is the one that the B operand has
+//     (head lane / 4, tokens 2 (lane % 4) and the next), so P needs no exchange
+//     between lanes.  P is rounded to fp16 once (2^-11).
+//   P stays within fp16: the softmax reference follows x_t + log2 of the
+//     largest scale of V among the chunk's tokens, and moves (with a rescale of
+//     the accumulators) only when a P could pass 2^15; it is put at 2^10 then,
+//     so that P is a normal number down to 2^-24 of the largest.
+// ldmatrix reads K rows (token, 16 bytes) as they lie; transposed, it pairs
+// two tokens of V in each register.  The pieces of 8 tokens are 128 contiguous
+// bytes, so both are free of bank conflicts.
 #pragma once
 
 #include <math.h>
 #include <stdint.h>
 
 #include "decode.cuh"
+#include "decode_gqa.cuh"
 #include "device_utils.cuh"
+#include "mma_utils.cuh"
 #include "quant4.cuh"
 
 namespace pa {
 
+constexpr int kQ4ChunkBlocks = 4;  // blocks a ring stage holds
+constexpr int kQ4Chunk = kQ4ChunkBlocks * kBlock;
+
 template <typename T, int D>
 struct Q4Config {
   static constexpr int WARPS = 4;
-  static constexpr int KVPI = 4;  // KV heads per work item, one warp each
   static constexpr int THREADS = WARPS * 32;
-  static size_t smem_bytes(int partition_size) { return (size_t)(partition_size / kBlock) * 4; }
+  static constexpr int TILE = q4_tile_bytes(D);
+  static constexpr int HALF = kQ4ChunkBlocks * TILE;  // the K (or V) tiles of a stage
+  static constexpr int STAGE_BYTES = 2 * HALF;
+  static constexpr int NSTAGE = D == 128 ? 2 : 4;
+  static_assert(STAGE_BYTES % 128 == 0, "stages start 128-byte aligned");
+  static size_t smem_bytes(int partition_size) {
+    return (size_t)WARPS * NSTAGE * STAGE_BYTES + (size_t)WARPS * NSTAGE * 8 +
+           (size_t)(partition_size / kBlock) * 4;
+  }
 };
 
-template <typename T, int D, int G, bool MASS>
-__global__ void __launch_bounds__(128) paged_decode_q4_kernel(DecodeArgs a) {
+// KV heads per work item: the CTA's four warps take four heads, or share two
+// heads or one where the pool has no more.
+inline int q4_heads_per_item(int heads) { return heads >= 4 ? 4 : heads >= 2 ? 2 : 1; }
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  Chunk<T>::to_float(*reinterpret_cast<const uint4*>(p), f);
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+constexpr uint32_t kMinus2m10 = 0x94009400u;  // -2^-10 in both halves
+
+// (n - z) 2^-10 of the numbers in bits 0-3 (even) or 4-7 (odd) of both halves,
+// given nz = -z 2^-10: exact.
+__device__ __forceinline__ uint32_t q4_even(uint32_t w, __half2 nz) {
+  return as_u32(__hfma2(as_half2(w & 0x000f000fu), as_half2(0x74007400u), nz));  // 2^14
+}
+__device__ __forceinline__ uint32_t q4_odd(uint32_t w, __half2 nz) {
+  return as_u32(__hfma2(as_half2(w & 0x00f000f0u), as_half2(0x64006400u), nz));  // 2^10
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) { return MmaType<__half>::pack(a, b); }
+
+template <typename T, int D, bool MASS>
+__global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, int heads_per_item) {
   using Cfg = Q4Config<T, D>;
-  constexpr int DPL = D / 32;  // dimensions per lane
-  constexpr int TILE = q4_tile_bytes(D);
-  extern __shared__ int32_t q4_tbl[];
-  __shared__ int32_t s_item, s_merge, s_plan_ok;
+  constexpr int TILE = Cfg::TILE, NSTAGE = Cfg::NSTAGE;
+  constexpr int PIECES = D / 32, GROUPS = D / 64;
+  constexpr int CB = kQ4ChunkBlocks;
+
+  extern __shared__ __align__(128) uint8_t q4_smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + Cfg::WARPS * NSTAGE * Cfg::STAGE_BYTES);
+  int32_t* tbl = reinterpret_cast<int32_t*>(bars + Cfg::WARPS * NSTAGE);
+  __shared__ int32_t s_item, s_abort, s_merge, s_plan_ok;
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int HK = a.heads, HQ = HK * G, PS = a.partition_size;
+  const int r = lane >> 2, j = lane & 3;  // fragment row (query head, or dimension) and quad lane
+  const int G = a.q_per_kv, HK = a.heads, HQ = HK * G, PS = a.partition_size;
+  const int wph = Cfg::WARPS / heads_per_item;  // warps that share a KV head
+  const int part = warp % wph;
 
   if (a.after_plan) grid_dependency_wait();
+  int32_t next = -1;  // thread 0: the next item, once reserved
   if (threadIdx.x == 0) {
-    s_plan_ok = plan_header_ok(a);
-    if (!s_plan_ok) atomicOr(a.err, PA_DEVERR_PLAN);
+    for (int i = 0; i < Cfg::WARPS * NSTAGE; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    mbar_init_fence();
+    s_abort = 0;
+    s_plan_ok = plan_header_ok(a);  // see the MHA kernel
+    if (s_plan_ok) next = atomicAdd(&a.plan->work_counter, 1);
+    else atomicOr(a.err, PA_DEVERR_PLAN);
   }
   __syncthreads();
   if (!s_plan_ok) return;
   const int32_t num_items = a.plan->num_items;
 
+  uint32_t fills = 0;
+  uint8_t* my_stages = q4_smem + warp * NSTAGE * Cfg::STAGE_BYTES;
+  uint64_t* my_bars = bars + warp * NSTAGE;
+
   for (;;) {
-    if (threadIdx.x == 0) s_item = atomicAdd(&a.plan->work_counter, 1);
+    if (threadIdx.x == 0) {
+      s_item = next >= 0 ? next : atomicAdd(&a.plan->work_counter, 1);
+      next = -1;
+    }
     __syncthreads();
     const int item = s_item;
-    if (item >= num_items) break;
+    if (item >= num_items || s_abort) break;
     PlanItem it;
-    if (!plan_item(a, item, &it)) {
+    if (!plan_item(a, item, &it)) {  // a damaged plan entry: report and skip the item
       if (threadIdx.x == 0) atomicOr(a.err, PA_DEVERR_PLAN);
       __syncthreads();
       continue;
@@ -64,74 +143,321 @@ __global__ void __launch_bounds__(128) paged_decode_q4_kernel(DecodeArgs a) {
         atomicOr(a.err, PA_DEVERR_BLOCK_ID);
         b = 0;
       }
-      q4_tbl[i] = b;
+      tbl[i] = b;
     }
     __syncthreads();
 
-    const int kvh = g * Cfg::KVPI + warp;
-    if (kvh < HK) {
-      const int64_t sh0 = (int64_t)s * HQ + kvh * G;
-      const int d0 = lane * DPL;
-      float q[G][DPL], acc[G][DPL], m_run[G], l_run[G];
+    const int kvh = g * heads_per_item + warp / wph;
+    const bool mine = kvh < HK;
+    const int64_t sh0 = (int64_t)s * HQ + kvh * G;
+    // the chunks of the partition that this warp takes
+    const int chunks = (nblk + CB - 1) / CB;
+    const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
+
+    float ref = -INFINITY, l_run = 0.f;  // of query head r
+    float o[PIECES][2][4];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        m_run[h] = -INFINITY;
-        l_run[h] = 0.f;
+    for (int c = 0; c < PIECES; ++c)
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) {
-          q[h][e] = (float)static_cast<const T*>(a.q)[(sh0 + h) * D + d0 + e] * a.scale_log2;
-          acc[h][e] = 0.f;
-        }
-      }
-      const int off = (d0 / 32) * 256 + (d0 % 32) / 2, word = q4_words_off(D) + (d0 / 64) * 64;
-      auto row = [&](const uint8_t* tile, int t, float* x) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + word + t * 4);
-        const float sc = q4_scale(w), z = q4_zero(w);
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int e = 0; e < DPL; e += 2) {
-          const uint32_t b = tile[off + t * 16 + e / 2];
-          x[e] = sc * ((float)(b & 15u) - z);
-          x[e + 1] = sc * ((float)(b >> 4) - z);
+        for (int e = 0; e < 4; ++e) o[c][m][e] = 0.f;
+
+    bool ok = true;
+    if (mine) {
+      const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pool) + (int64_t)kvh * TILE;
+      const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pool) + (int64_t)kvh * TILE;
+      const int64_t block_bytes = (int64_t)HK * TILE;
+      // fill k with chunk c: lanes 0 .. 7 copy the K and V tiles of its blocks
+      auto issue = [&](uint32_t k, int c) {
+        const int st = k % NSTAGE;
+        const uint32_t bar = smem_addr(&my_bars[st]);
+        const int nb = min(CB, nblk - c * CB);
+        __syncwarp();  // every lane is done with the stage
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nb * 2 * TILE));
+        __syncwarp();
+        if (lane < 2 * nb) {
+          fence_proxy_async_shared();
+          const int b = lane >> 1;
+          const int64_t off = (int64_t)tbl[c * CB + b] * block_bytes;
+          const uint32_t dst = smem_addr(my_stages + st * Cfg::STAGE_BYTES) + (lane & 1) * Cfg::HALF + b * TILE;
+          bulk_copy_g2s(dst, ((lane & 1) ? vbase : kbase) + off, TILE, bar);
         }
       };
-      for (int i = 0; i < nblk; ++i) {
-        const int64_t at = ((int64_t)q4_tbl[i] * HK + kvh) * TILE;
-        const uint8_t* kt = static_cast<const uint8_t*>(a.k_pool) + at;
-        const uint8_t* vt = static_cast<const uint8_t*>(a.v_pool) + at;
-        const int valid = min(kBlock, ntok - i * kBlock);
-        for (int t = 0; t < valid; ++t) {
-          float k[DPL], v[DPL];
-          row(kt, t, k);
-          row(vt, t, v);
+      const uint32_t k0 = fills;
+      for (int i = 0; i < NSTAGE && i < c_n; ++i) issue(k0 + i, c_lo + i);
+
+      // Q fragments (rows >= G are zero), scaled by 2^qe so that the row's
+      // largest value lies in [2^14, 2^15)
+      uint32_t qa[PIECES][4];  // two k-steps of (a0, a2)
+      float kq;                // raw score to log2 units
+      {
+        float qf[PIECES][8], top = 0.f;
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            float x = 0.f;
+        for (int c = 0; c < PIECES; ++c) {
+          if (r < G) {
+            load8(static_cast<const T*>(a.q) + (sh0 + r) * D + 32 * c + 8 * j, qf[c]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < DPL; ++e) x = fmaf(q[h][e], k[e], x);
+            for (int e = 0; e < 8; ++e) qf[c][e] = 0.f;
+          }
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
-            if (MASS && lane == 0) a.scores[(sh0 + h) * a.score_stride + tok0 + i * kBlock + t] = x;
-            const float m_new = fmaxf(m_run[h], x);
-            const float alpha = exp2f(m_run[h] - m_new), w = exp2f(x - m_new);
-            m_run[h] = m_new;
-            l_run[h] = fmaf(l_run[h], alpha, w);
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(qf[c][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+        const int ex = (int)(__float_as_uint(top) >> 23);  // biased exponent; 255: infinity or NaN
+        const int qe = ex == 255 ? 0 : min(14 + 127 - ex, 100);
+        const float f = __uint_as_float((uint32_t)(qe + 127) << 23);
+        kq = a.scale_log2 * __uint_as_float((uint32_t)(127 + 10 - qe) << 23);  // 2^(10 - qe)
 #pragma unroll
-            for (int e = 0; e < DPL; ++e) acc[h][e] = fmaf(acc[h][e], alpha, w * v[e]);
+        for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // pairs as the nibbles lie in a register: (0, 4), (1, 5), ...
+            qa[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
+      }
+
+      int i = 0;
+      for (; i < c_n; ++i) {
+        const uint32_t k = k0 + i;
+        const int st = k % NSTAGE;
+        if (!__all_sync(kFullMask, mbar_wait_bounded(smem_addr(&my_bars[st]), (k / NSTAGE) & 1u))) {
+          ok = false;
+          break;
+        }
+        uint8_t* kt = my_stages + st * Cfg::STAGE_BYTES;
+        uint8_t* vt = kt + Cfg::HALF;
+        const int valid = min(kQ4Chunk, ntok - (c_lo + i) * kQ4Chunk);
+        if (valid < kQ4Chunk) {
+          // slots past the context hold anything: their V words become zero
+          // (scale and zero point), so that they add nothing; their scores
+          // are masked below
+          for (int t = valid + lane; t < kQ4Chunk; t += 32)
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr)
+              *reinterpret_cast<uint32_t*>(vt + (t >> 4) * TILE + q4_words_off(D) + (gr * 16 + (t & 15)) * 4) = 0u;
+          __syncwarp();
+        }
+
+        // ---- scores of the chunk: x[b][nt][e] of head r, token 16 b + 8 nt + 2 j + e
+        float x[CB][2][2];
+#pragma unroll
+        for (int b = 0; b < CB; ++b) {
+          const uint32_t tile = smem_addr(kt + b * TILE);
+          uint32_t kw[2][PIECES];
+          if constexpr (D == 128) {
+            const uint32_t at = tile + (lane >> 3) * 256 + (lane & 7) * 16;
+            ldmatrix_x4(kw[0], at);
+            ldmatrix_x4(kw[1], at + 128);
+          } else {
+            uint32_t w[4];
+            ldmatrix_x4(w, tile + ((lane >> 3) & 1) * 256 + (lane >> 4) * 128 + (lane & 7) * 16);
+            kw[0][0] = w[0], kw[0][1] = w[1], kw[1][0] = w[2], kw[1][1] = w[3];
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint8_t* words = kt + b * TILE + q4_words_off(D) + nt * 32;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) {
+              // -z 2^-10 of the operand's token, in both halves
+              const uint32_t zw = *reinterpret_cast<const uint32_t*>(words + gr * 64 + r * 4);
+              const __half2 nz = __hmul2(as_half2(__byte_perm(zw, zw, 0x1010)), as_half2(kMinus2m10));
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
+                const uint32_t w = kw[nt][pc], w8 = w >> 8;
+                const uint32_t a0[4] = {qa[pc][0], 0u, qa[pc][1], 0u};
+                const uint32_t a1[4] = {qa[pc][2], 0u, qa[pc][3], 0u};
+                mma16816<__half>(c, a0, q4_even(w, nz), q4_odd(w, nz));
+                mma16816<__half>(c, a1, q4_even(w8, nz), q4_odd(w8, nz));
+              }
+              const uint2 sc = *reinterpret_cast<const uint2*>(words + gr * 64 + j * 8);
+              sum0 = fmaf(q4_scale(sc.x), c[0], sum0);
+              sum1 = fmaf(q4_scale(sc.y), c[1], sum1);
+            }
+            x[b][nt][0] = sum0 * kq;
+            x[b][nt][1] = sum1 * kq;
+          }
+        }
+        if (valid < kQ4Chunk) {
+#pragma unroll
+          for (int b = 0; b < CB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (b * 16 + nt * 8 + 2 * j + e >= valid) x[b][nt][e] = -INFINITY;
+        }
+        if constexpr (MASS) {
+          if (r < G) {
+            const int t0 = (c_lo + i) * kQ4Chunk + 2 * j;
+            float* dst = a.scores + (sh0 + r) * a.score_stride + tok0 + t0;
+#pragma unroll
+            for (int b = 0; b < CB; ++b)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (b * 16 + nt * 8 + 2 * j + e < valid) dst[b * 16 + nt * 8 + e] = x[b][nt][e];
+          }
+        }
+
+        // ---- softmax: the chunk's maximum and its largest V scale
+        float mx = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < CB; ++b)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) mx = fmaxf(mx, fmaxf(x[b][nt][0], x[b][nt][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+        uint32_t big = 0u;
+        constexpr int WPB = 4 * GROUPS;  // 16-byte loads that hold a block's words
+        if (lane < CB * WPB) {
+          const uint4 w = *reinterpret_cast<const uint4*>(vt + (lane / WPB) * TILE + q4_words_off(D) +
+                                                          (lane % WPB) * 16);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (ws[e] < 0x7f800000u) big = max(big, ws[e]);  // NaN scales do not count
+        }
+        big = __reduce_max_sync(kFullMask, big);
+        const float y = mx + (float)max((int)(big >> 23) - 127, -100);
+        const bool move = y > ref + 14.f;
+        if (__any_sync(kFullMask, move)) {
+          float alpha = 1.f;
+          if (move) {
+            alpha = exp2f(ref - (y - 10.f));  // 0 on the first move
+            ref = y - 10.f;
+          }
+          l_run *= alpha;
+          const float al0 = __shfl_sync(kFullMask, alpha, 8 * j), al1 = __shfl_sync(kFullMask, alpha, 8 * j + 4);
+#pragma unroll
+          for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[c][m][e] *= (e & 1) ? al1 : al0;
+        }
+        const float mb = ref == -INFINITY ? 0.f : ref;
+
+        // ---- values
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < CB; ++b) {
+          float w[2][2];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              w[nt][e] = exp2f(x[b][nt][e] - mb);
+              sum += w[nt][e];
+            }
+          const uint32_t tile = smem_addr(vt + b * TILE);
+#pragma unroll
+          for (int gr = 0; gr < GROUPS; ++gr) {
+            uint32_t pb[2];
+            __half2 nz[2];  // -z 2^-10 of the two tokens
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const uint2 words = *reinterpret_cast<const uint2*>(
+                  vt + b * TILE + q4_words_off(D) + (gr * 16 + nt * 8 + 2 * j) * 4);
+              pb[nt] = pack_half(w[nt][0] * q4_scale(words.x), w[nt][1] * q4_scale(words.y));
+              nz[nt] = __hmul2(as_half2(__byte_perm(words.x, words.y, 0x5410)), as_half2(kMinus2m10));
+            }
+            uint32_t v[4];
+            ldmatrix_x4_trans(v, tile + (2 * gr + (lane >> 4)) * 256 + ((lane >> 3) & 1) * 128 + (lane & 7) * 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t v0 = v[2 * h], v1 = v[2 * h + 1], u0 = v0 >> 8, u1 = v1 >> 8;
+              const uint32_t a0[4] = {q4_even(v0, nz[0]), q4_odd(v0, nz[0]), q4_even(v1, nz[1]), q4_odd(v1, nz[1])};
+              const uint32_t a1[4] = {q4_even(u0, nz[0]), q4_odd(u0, nz[0]), q4_even(u1, nz[1]), q4_odd(u1, nz[1])};
+              mma16816<__half>(o[2 * gr + h][0], a0, pb[0], pb[1]);
+              mma16816<__half>(o[2 * gr + h][1], a1, pb[0], pb[1]);
+            }
+          }
+        }
+        sum += __shfl_xor_sync(kFullMask, sum, 1);
+        sum += __shfl_xor_sync(kFullMask, sum, 2);
+        l_run += sum;
+        if (i + NSTAGE < c_n) issue(k + NSTAGE, c_lo + i + NSTAGE);
+        // as in the MHA kernel: the next item is reserved shortly before this one ends
+        if (threadIdx.x == 0 && i == max(c_n - 2, 0)) next = atomicAdd(&a.plan->work_counter, 1);
+      }
+      if (!ok) {
+        if (lane == 0) {  // as in the MHA kernel: report, stop, and poison the plan
+          atomicOr(a.err, PA_DEVERR_TIMEOUT);
+          s_abort = 1;
+          a.plan->poisoned = 1;
+          __threadfence();
+        }
+        const int issued = min(c_n, i + NSTAGE);
+        for (int jj = i; jj < issued; ++jj) {
+          const uint32_t k = k0 + jj;
+          mbar_wait_bounded(smem_addr(&my_bars[k % NSTAGE]), (k / NSTAGE) & 1u);
+        }
+      } else {
+        fills = k0 + c_n;
+      }
+      if (wph > 1 && part > 0) {  // for the first warp of the head (this warp's stages are drained)
+        float* xs = reinterpret_cast<float*>(my_stages);
+#pragma unroll
+        for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xs[((c * 2 + m) * 4 + e) * 32 + lane] = o[c][m][e];
+        xs[PIECES * 8 * 32 + lane] = ref;
+        xs[(PIECES * 8 + 1) * 32 + lane] = l_run;
+        fence_proxy_async_shared();  // before the ring's next bulk copies into the same bytes
+      }
+    }
+    if (wph > 1) __syncthreads();
+    if (mine && part == 0 && (wph > 1 ? !s_abort : ok)) {
+      for (int other = 1; other < wph; ++other) {  // fold in the other warps' states
+        const float* xs = reinterpret_cast<const float*>(my_stages + other * NSTAGE * Cfg::STAGE_BYTES);
+        const float rb = xs[PIECES * 8 * 32 + lane], lb = xs[(PIECES * 8 + 1) * 32 + lane];
+        const float M = fmaxf(ref, rb);
+        const float sa = ref == -INFINITY ? 0.f : exp2f(ref - M);
+        const float sb = rb == -INFINITY ? 0.f : exp2f(rb - M);
+        const float sa0 = __shfl_sync(kFullMask, sa, 8 * j), sa1 = __shfl_sync(kFullMask, sa, 8 * j + 4);
+        const float sb0 = __shfl_sync(kFullMask, sb, 8 * j), sb1 = __shfl_sync(kFullMask, sb, 8 * j + 4);
+#pragma unroll
+        for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[c][m][e] = o[c][m][e] * ((e & 1) ? sa1 : sa0) +
+                           xs[((c * 2 + m) * 4 + e) * 32 + lane] * ((e & 1) ? sb1 : sb0);
+        l_run = l_run * sa + lb * sb;
+        ref = M;
+      }
+      if (wph > 1) fence_proxy_async_shared();  // the other warps' rings are refilled after the loop's barrier
+      // this lane holds dimensions 32 c + 4 r .. + 3 of heads 2 j and 2 j + 1
+      // the accumulators hold 2^-10 of their sums
+      const float inv = split ? 1024.f : ref != -INFINITY ? 1024.f / l_run : 0.f;
+      const float inv2[2] = {__shfl_sync(kFullMask, inv, 8 * j), __shfl_sync(kFullMask, inv, 8 * j + 4)};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * j + e;
+        if (h >= G) continue;
+#pragma unroll
+        for (int c = 0; c < PIECES; ++c) {
+          const float v[4] = {o[c][0][e] * inv2[e], o[c][0][2 + e] * inv2[e], o[c][1][e] * inv2[e],
+                              o[c][1][2 + e] * inv2[e]};
+          if (!split) {
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
+                make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
+          } else {
+            *reinterpret_cast<float4*>(a.part_acc + ((sh0 + h) * a.max_parts + p) * D + 32 * c + 4 * r) =
+                make_float4(v[0], v[1], v[2], v[3]);
           }
         }
       }
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        if (!split) {
-          const float inv = nblk > 0 ? 1.f / l_run[h] : 0.f;
-#pragma unroll
-          for (int e = 0; e < DPL; ++e) static_cast<T*>(a.out)[(sh0 + h) * D + d0 + e] = (T)(acc[h][e] * inv);
-          if (MASS && lane == 0) a.lse[sh0 + h] = m_run[h] + log2f(l_run[h]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < DPL; ++e) a.part_acc[((sh0 + h) * a.max_parts + p) * D + d0 + e] = acc[h][e];
-          if (lane == 0) a.part_ml[(sh0 + h) * a.max_parts + p] = make_float2(m_run[h], l_run[h]);
-        }
+      if (j == 0 && r < G) {
+        if (split) a.part_ml[(sh0 + r) * a.max_parts + p] = make_float2(ref, l_run);
+        else if (MASS) a.lse[sh0 + r] = ref + log2f(l_run);
       }
     }
     if (split) {
@@ -141,14 +467,31 @@ __global__ void __launch_bounds__(128) paged_decode_q4_kernel(DecodeArgs a) {
         __threadfence();
         const int arrived = atomicAdd(cnt, 1) + 1;
         __threadfence();
-        s_merge = arrived == ni && *(volatile int32_t*)&a.plan->poisoned == 0;
+        s_merge = arrived == ni && !s_abort && *(volatile int32_t*)&a.plan->poisoned == 0;
         if (arrived == ni) *cnt = 0;
       }
       __syncthreads();
-      if (s_merge && kvh < HK) {
+      if (s_merge && mine && part == 0) {
         __threadfence();
-        for (int h = 0; h < G; ++h)
-          merge_partitions<T, D, MASS>(a, (int64_t)s * HQ + kvh * G + h, np, lane);
+        // rounds of at most 8 partitions of every head (each keeps its weights in registers)
+        constexpr int RING = NSTAGE * Cfg::STAGE_BYTES, ROUND = 8 * D * 4;
+        constexpr auto buf = [](int g) { return g * ROUND < RING ? g * ROUND : RING; };
+        bool merged = true;
+        if (G == 1) {
+          const int used = merge_staged<T, D, NSTAGE, RING, MASS>(a, sh0, np, lane, my_stages, my_bars, fills);
+          fills += used > 0 ? used : -used;
+          merged = used > 0;
+        } else {
+          merged = G == 8   ? merge_group<T, D, 8, NSTAGE, buf(8), MASS>(a, sh0, np, lane, my_stages, my_bars, fills)
+                   : G == 4 ? merge_group<T, D, 4, NSTAGE, buf(4), MASS>(a, sh0, np, lane, my_stages, my_bars, fills)
+                            : merge_group<T, D, 2, NSTAGE, buf(2), MASS>(a, sh0, np, lane, my_stages, my_bars, fills);
+        }
+        if (!merged && lane == 0) {  // as for a copy of the item: report, stop, poison the plan
+          atomicOr(a.err, PA_DEVERR_TIMEOUT);
+          s_abort = 1;
+          a.plan->poisoned = 1;
+          __threadfence();
+        }
       }
     }
     __syncthreads();

@@ -147,7 +147,7 @@ int64_t block_bytes(const pa_pool* pool) {
 }
 
 int kv_heads_per_item(const pa_pool* pool) {
-  if (is_q4(pool)) return Q4Config<__half, 128>::KVPI;
+  if (is_q4(pool)) return q4_heads_per_item(pool->heads);
   return use_gqa_mma(pool) ? GqaConfig<__half, 128, kGqaStages>::KVPI : rings_for(pool->q_per_kv);
 }
 
@@ -278,6 +278,16 @@ cudaError_t launch_gqa(const DecodeArgs& a, const DeviceState& dev, cudaStream_t
   return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap, tm_k, tm_v);
 }
 
+template <typename T, int D>
+cudaError_t set_q4_attrs() {
+  const int smem = (int)Q4Config<T, D>::smem_bytes(kMaxPartition);
+  const cudaError_t e = cudaFuncSetAttribute(paged_decode_q4_kernel<T, D, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_decode_q4_kernel<T, D, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 // Once per device, with that device current: resolve the error word's device
 // address and raise the shared-memory limit of the decode kernels.
 pa_status device_state(DeviceState** out) {
@@ -311,6 +321,10 @@ pa_status device_state(DeviceState** out) {
                            set_gqa_attrs<__half, 128>(),
                            set_gqa_attrs<__nv_bfloat16, 64>(),
                            set_gqa_attrs<__nv_bfloat16, 128>(),
+                           set_q4_attrs<__half, 64>(),
+                           set_q4_attrs<__half, 128>(),
+                           set_q4_attrs<__nv_bfloat16, 64>(),
+                           set_q4_attrs<__nv_bfloat16, 128>(),
                            set_prefill_attrs<__half, 64>(),
                            set_prefill_attrs<__half, 128>(),
                            set_prefill_attrs<__nv_bfloat16, 64>(),
@@ -454,10 +468,10 @@ cudaError_t launch_decode(const DecodeArgs& a, const DeviceState& dev, cudaStrea
   return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap);
 }
 
-template <typename T, int D, int G>
+template <typename T, int D>
 cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream, bool overlap) {
   using Cfg = Q4Config<T, D>;
-  auto kernel = a.scores ? paged_decode_q4_kernel<T, D, G, true> : paged_decode_q4_kernel<T, D, G, false>;
+  auto kernel = a.scores ? paged_decode_q4_kernel<T, D, true> : paged_decode_q4_kernel<T, D, false>;
   const size_t smem = Cfg::smem_bytes(a.partition_size);
   int per_sm = 0;
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);
@@ -465,18 +479,7 @@ cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t 
   per_sm = std::max(per_sm, 1);
   const int64_t upper = (int64_t)a.num_seqs * a.max_parts * a.head_groups;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(upper, (int64_t)dev.num_sms * per_sm));
-  return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap);
-}
-
-template <typename T, int D>
-cudaError_t launch_q4_grouped(int G, const DecodeArgs& a, const DeviceState& dev, cudaStream_t s,
-                              bool overlap) {
-  switch (G) {
-    case 1: return launch_q4<T, D, 1>(a, dev, s, overlap);
-    case 2: return launch_q4<T, D, 2>(a, dev, s, overlap);
-    case 4: return launch_q4<T, D, 4>(a, dev, s, overlap);
-    default: return launch_q4<T, D, 8>(a, dev, s, overlap);
-  }
+  return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap, q4_heads_per_item(a.heads));
 }
 
 template <typename T, int D>
@@ -820,13 +823,13 @@ pa_status launch_run(const pa_pool* pool, const DecodeArgs& a, const DeviceState
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode launch");
   }
   switch (pool->dtype * 1000 + pool->head_dim) {
-    case PA_Q4_F16 * 1000 + 64: e = launch_q4_grouped<__half, 64>(pool->q_per_kv, a, dev, s, overlap); break;
-    case PA_Q4_F16 * 1000 + 128: e = launch_q4_grouped<__half, 128>(pool->q_per_kv, a, dev, s, overlap); break;
+    case PA_Q4_F16 * 1000 + 64: e = launch_q4<__half, 64>(a, dev, s, overlap); break;
+    case PA_Q4_F16 * 1000 + 128: e = launch_q4<__half, 128>(a, dev, s, overlap); break;
     case PA_Q4_BF16 * 1000 + 64:
-      e = launch_q4_grouped<__nv_bfloat16, 64>(pool->q_per_kv, a, dev, s, overlap);
+      e = launch_q4<__nv_bfloat16, 64>(a, dev, s, overlap);
       break;
     case PA_Q4_BF16 * 1000 + 128:
-      e = launch_q4_grouped<__nv_bfloat16, 128>(pool->q_per_kv, a, dev, s, overlap);
+      e = launch_q4<__nv_bfloat16, 128>(a, dev, s, overlap);
       break;
     case PA_F32 * 1000 + 64: e = launch_grouped<float, 64>(pool->q_per_kv, a, dev, s, overlap); break;
     case PA_F32 * 1000 + 128: e = launch_grouped<float, 128>(pool->q_per_kv, a, dev, s, overlap); break;

@@ -7,7 +7,9 @@ Tolerance of the attention, from the arithmetic (D dimensions, N tokens):
   2^-25 of the largest where it is subnormal.  A score is an fp32 sum of D products
   and of the zero point's term, off by at most D 2^-24 scale sum |q| s (n + |z|) =: e;
   with the exponential's own 2^-22 that moves a weight by a factor of 1 + e + 2^-22,
-  in the numerator and in the denominator.
+  in the numerator and in the denominator.  The numerator is an fp32 sum of N
+  products, each of which enters a partial sum by rounding or chopping, at most 2^-23 of it:
+  off by at most N 2^-23 sum_t w |v|.
 """
 import math
 
@@ -242,7 +244,7 @@ def reference(c):
             vals = np.stack([v[c["tables"][i, t // 16], hk, t % 16] for t in range(L)])
             e = c["dim"] * 2.0 ** -24 * c["scale"] * (rows @ np.abs(c["qx"][i, h])).max() + 2.0 ** -22
             tol[i, h] = (eps / 2 * np.abs(out[i, h]) * 1.01 + (1.01 * 2.0 ** -11 + 2 * e) * bound[i, h]
-                         + L * 2.0 ** -25 * np.abs(vals).max() + torch.finfo(TYPES[c["kind"]][0]).smallest_normal * eps)
+                         + L * 2.0 ** -23 * bound[i, h] + L * 2.0 ** -25 * np.abs(vals).max() + torch.finfo(TYPES[c["kind"]][0]).smallest_normal * eps)
     return out, tol, weights
 
 
