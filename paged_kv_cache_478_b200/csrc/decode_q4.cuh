@@ -13,13 +13,15 @@
 // sum by the exponents its operands are written with: subnormals cost it 6 to 10
 // bits (measured: sums off by 2^-18 of their terms).
 //   scores:  x_t = sum_g s_t,g sum_d q_d (n_t,d - z_t,g), g a group of 64 dimensions.
-//     Q is the A operand (16 rows, G of them used), scaled by a power of two
-//     into fp16's range (exact for fp16 and bf16 queries).
+//     K is the A operand (16 tokens), Q the B operand (8 columns, G of them
+//     used), scaled by a power of two into fp16's range (exact for fp16 and
+//     bf16 queries).  A lane gets the scores of tokens lane / 4 and lane / 4 + 8
+//     of each block and of heads 2 (lane % 4) and the next, so that one word a
+//     token and group gives both its zero point and its scale.
 //   values:  o_d = sum_t P_t,g (n_t,d - z_t,g),  P_t,g = w_t s_t,g.
-//     V^T is the A operand, P the B operand: the layout in which the scores'
-//     accumulators leave the tensor cores is the one that the B operand has
-//     (head lane / 4, tokens 2 (lane % 4) and the next), so P needs no exchange
-//     between lanes.  P is rounded to fp16 once (2^-11).
+//     V^T is the A operand; P, rounded to fp16 once (2^-11) and transposed 8 x 8
+//     by movmatrix, the B operand, so its accumulators belong to the same two
+//     heads as the lane's softmax state.
 //   P stays within fp16: the softmax reference follows x_t + log2 of the
 //     largest scale of V among the chunk's tokens, and moves (with a rescale of
 //     the accumulators) only when a P could pass 2^15; it is put at 2^10 then,
@@ -81,7 +83,22 @@ __device__ __forceinline__ uint32_t q4_odd(uint32_t w, __half2 nz) {
 }
 __device__ __forceinline__ uint32_t pack_half(float a, float b) { return MmaType<__half>::pack(a, b); }
 
-template <typename T, int D, bool MASS>
+// One 8 x 8 matrix of 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// 2^x; results below the normal numbers become zero.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// NH: query heads a lane keeps scores of: 2, or 1 where G is 1.
+template <typename T, int D, int NH, bool MASS>
 __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, int heads_per_item) {
   using Cfg = Q4Config<T, D>;
   constexpr int TILE = Cfg::TILE, NSTAGE = Cfg::NSTAGE;
@@ -154,7 +171,9 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     const int chunks = (nblk + CB - 1) / CB;
     const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
 
-    float ref = -INFINITY, l_run = 0.f;  // of query head r
+    float ref[NH], l_run[NH];  // of query heads 2 j and 2 j + 1; l_run over this lane's tokens
+#pragma unroll
+    for (int e = 0; e < NH; ++e) ref[e] = -INFINITY, l_run[e] = 0.f;
     float o[PIECES][2][4];
 #pragma unroll
     for (int c = 0; c < PIECES; ++c)
@@ -189,8 +208,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 
       // Q fragments (rows >= G are zero), scaled by 2^qe so that the row's
       // largest value lies in [2^14, 2^15)
-      uint32_t qa[PIECES][4];  // two k-steps of (a0, a2)
-      float kq;                // raw score to log2 units
+      uint32_t qb[PIECES][4];  // two k-steps of (b0, b1): head r, dimensions 32 c + 8 j .. + 7
+      float kq[NH];            // raw scores to log2 units, positive: a negative scale turns Q
       {
         float qf[PIECES][8], top = 0.f;
 #pragma unroll
@@ -208,13 +227,17 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
         const int ex = (int)(__float_as_uint(top) >> 23);  // biased exponent; 255: infinity or NaN
         const int qe = ex == 255 ? 0 : min(14 + 127 - ex, 100);
-        const float f = __uint_as_float((uint32_t)(qe + 127) << 23);
-        kq = a.scale_log2 * __uint_as_float((uint32_t)(127 + 10 - qe) << 23);  // 2^(10 - qe)
+        const float f = copysignf(__uint_as_float((uint32_t)(qe + 127) << 23), a.scale_log2);
+        // 2^(10 - qe); never zero, so that a masked score stays -infinity when the scale is 0
+        const float mine_kq = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + 10 - qe) << 23),
+                                    1.17549435e-38f);
+#pragma unroll
+        for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 8 * j + 4 * e);
 #pragma unroll
         for (int c = 0; c < PIECES; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e)  // pairs as the nibbles lie in a register: (0, 4), (1, 5), ...
-            qa[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
+            qb[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
       }
 
       int i = 0;
@@ -239,8 +262,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           __syncwarp();
         }
 
-        // ---- scores of the chunk: x[b][nt][e] of head r, token 16 b + 8 nt + 2 j + e
-        float x[CB][2][2];
+        // ---- raw scores of the chunk: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e
+        float x[CB][2][NH];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
           const uint32_t tile = smem_addr(kt + b * TILE);
@@ -254,30 +277,32 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             ldmatrix_x4(w, tile + ((lane >> 3) & 1) * 256 + (lane >> 4) * 128 + (lane & 7) * 16);
             kw[0][0] = w[0], kw[0][1] = w[1], kw[1][0] = w[2], kw[1][1] = w[3];
           }
+          const uint8_t* words = kt + b * TILE + q4_words_off(D) + r * 4;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint8_t* words = kt + b * TILE + q4_words_off(D) + nt * 32;
-            float sum0 = 0.f, sum1 = 0.f;
+          for (int gr = 0; gr < GROUPS; ++gr) {
+            uint32_t word[2];
+            __half2 nz[2];  // -z 2^-10 of the two tokens, in both halves
 #pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr) {
-              // -z 2^-10 of the operand's token, in both halves
-              const uint32_t zw = *reinterpret_cast<const uint32_t*>(words + gr * 64 + r * 4);
-              const __half2 nz = __hmul2(as_half2(__byte_perm(zw, zw, 0x1010)), as_half2(kMinus2m10));
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
-                const uint32_t w = kw[nt][pc], w8 = w >> 8;
-                const uint32_t a0[4] = {qa[pc][0], 0u, qa[pc][1], 0u};
-                const uint32_t a1[4] = {qa[pc][2], 0u, qa[pc][3], 0u};
-                mma16816<__half>(c, a0, q4_even(w, nz), q4_odd(w, nz));
-                mma16816<__half>(c, a1, q4_even(w8, nz), q4_odd(w8, nz));
-              }
-              const uint2 sc = *reinterpret_cast<const uint2*>(words + gr * 64 + j * 8);
-              sum0 = fmaf(q4_scale(sc.x), c[0], sum0);
-              sum1 = fmaf(q4_scale(sc.y), c[1], sum1);
+            for (int nt = 0; nt < 2; ++nt) {
+              word[nt] = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
+              nz[nt] = __hmul2(as_half2(__byte_perm(word[nt], word[nt], 0x1010)), as_half2(kMinus2m10));
             }
-            x[b][nt][0] = sum0 * kq;
-            x[b][nt][1] = sum1 * kq;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
+              const uint32_t w0 = kw[0][pc], w1 = kw[1][pc], u0 = w0 >> 8, u1 = w1 >> 8;
+              const uint32_t a0[4] = {q4_even(w0, nz[0]), q4_even(w1, nz[1]), q4_odd(w0, nz[0]), q4_odd(w1, nz[1])};
+              const uint32_t a1[4] = {q4_even(u0, nz[0]), q4_even(u1, nz[1]), q4_odd(u0, nz[0]), q4_odd(u1, nz[1])};
+              mma16816<__half>(c, a0, qb[pc][0], qb[pc][1]);
+              mma16816<__half>(c, a1, qb[pc][2], qb[pc][3]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < NH; ++e) {
+                const float sc = q4_scale(word[nt]);
+                x[b][nt][e] = gr == 0 ? sc * c[2 * nt + e] : fmaf(sc, c[2 * nt + e], x[b][nt][e]);
+              }
           }
         }
         if (valid < kQ4Chunk) {
@@ -285,32 +310,34 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int b = 0; b < CB; ++b)
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
+              if (b * 16 + nt * 8 + r >= valid) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (b * 16 + nt * 8 + 2 * j + e >= valid) x[b][nt][e] = -INFINITY;
+                for (int e = 0; e < NH; ++e) x[b][nt][e] = -INFINITY;
+              }
         }
         if constexpr (MASS) {
-          if (r < G) {
-            const int t0 = (c_lo + i) * kQ4Chunk + 2 * j;
-            float* dst = a.scores + (sh0 + r) * a.score_stride + tok0 + t0;
+#pragma unroll
+          for (int e = 0; e < NH; ++e) {
+            if (2 * j + e >= G) continue;
+            float* dst = a.scores + (sh0 + 2 * j + e) * a.score_stride + tok0 + (c_lo + i) * kQ4Chunk + r;
 #pragma unroll
             for (int b = 0; b < CB; ++b)
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (b * 16 + nt * 8 + 2 * j + e < valid) dst[b * 16 + nt * 8 + e] = x[b][nt][e];
+                if (b * 16 + nt * 8 + r < valid) dst[b * 16 + nt * 8] = x[b][nt][e] * kq[e];
           }
         }
 
-        // ---- softmax: the chunk's maximum and its largest V scale
-        float mx = -INFINITY;
+        // ---- softmax: the chunk's maxima and its largest V scale
+        float mx[NH];
 #pragma unroll
-        for (int b = 0; b < CB; ++b)
+        for (int e = 0; e < NH; ++e) {
+          mx[e] = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) mx = fmaxf(mx, fmaxf(x[b][nt][0], x[b][nt][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+          for (int b = 0; b < CB; ++b) mx[e] = fmaxf(mx[e], fmaxf(x[b][0][e], x[b][1][e]));
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFullMask, mx[e], m));
+        }
         uint32_t big = 0u;
         constexpr int WPB = 4 * GROUPS;  // 16-byte loads that hold a block's words
         if (lane < CB * WPB) {
@@ -322,48 +349,57 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             if (ws[e] < 0x7f800000u) big = max(big, ws[e]);  // NaN scales do not count
         }
         big = __reduce_max_sync(kFullMask, big);
-        const float y = mx + (float)max((int)(big >> 23) - 127, -100);
-        const bool move = y > ref + 14.f;
+        const float ev = (float)max((int)(big >> 23) - 127, -100);
+        float y[NH];
+        bool move = false;
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          y[e] = fmaf(mx[e], kq[e], ev);
+          move |= y[e] > ref[e] + 14.f;
+        }
         if (__any_sync(kFullMask, move)) {
-          float alpha = 1.f;
-          if (move) {
-            alpha = exp2f(ref - (y - 10.f));  // 0 on the first move
-            ref = y - 10.f;
-          }
-          l_run *= alpha;
-          const float al0 = __shfl_sync(kFullMask, alpha, 8 * j), al1 = __shfl_sync(kFullMask, alpha, 8 * j + 4);
+          float alpha[2] = {1.f, 1.f};
+#pragma unroll
+          for (int e = 0; e < NH; ++e)
+            if (y[e] > ref[e] + 14.f) {
+              alpha[e] = ex2(ref[e] - (y[e] - 10.f));  // 0 on the first move
+              ref[e] = y[e] - 10.f;
+              l_run[e] *= alpha[e];
+            }
 #pragma unroll
           for (int c = 0; c < PIECES; ++c)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[c][m][e] *= (e & 1) ? al1 : al0;
+              for (int e = 0; e < 4; ++e) o[c][m][e] *= alpha[e & 1];
         }
-        const float mb = ref == -INFINITY ? 0.f : ref;
+        float mb[NH];
+#pragma unroll
+        for (int e = 0; e < NH; ++e) mb[e] = ref[e] == -INFINITY ? 0.f : -ref[e];
 
         // ---- values
-        float sum = 0.f;
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
-          float w[2][2];
+          float w[2][NH];
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              w[nt][e] = exp2f(x[b][nt][e] - mb);
-              sum += w[nt][e];
+            for (int e = 0; e < NH; ++e) {
+              w[nt][e] = ex2(fmaf(x[b][nt][e], kq[e], mb[e]));
+              l_run[e] += w[nt][e];
             }
           const uint32_t tile = smem_addr(vt + b * TILE);
+          const uint8_t* words = vt + b * TILE + q4_words_off(D);
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
             uint32_t pb[2];
-            __half2 nz[2];  // -z 2^-10 of the two tokens
+            __half2 nz[2];  // -z 2^-10 of tokens 2 j and 2 j + 1
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              const uint2 words = *reinterpret_cast<const uint2*>(
-                  vt + b * TILE + q4_words_off(D) + (gr * 16 + nt * 8 + 2 * j) * 4);
-              pb[nt] = pack_half(w[nt][0] * q4_scale(words.x), w[nt][1] * q4_scale(words.y));
-              nz[nt] = __hmul2(as_half2(__byte_perm(words.x, words.y, 0x5410)), as_half2(kMinus2m10));
+              const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
+              pb[nt] = movmatrix(pack_half(w[nt][0] * sc, NH == 2 ? w[nt][NH - 1] * sc : 0.f));
+              const uint2 two = *reinterpret_cast<const uint2*>(words + gr * 64 + nt * 32 + j * 8);
+              nz[nt] = __hmul2(as_half2(__byte_perm(two.x, two.y, 0x5410)), as_half2(kMinus2m10));
             }
             uint32_t v[4];
             ldmatrix_x4_trans(v, tile + (2 * gr + (lane >> 4)) * 256 + ((lane >> 3) & 1) * 128 + (lane & 7) * 16);
@@ -377,9 +413,6 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             }
           }
         }
-        sum += __shfl_xor_sync(kFullMask, sum, 1);
-        sum += __shfl_xor_sync(kFullMask, sum, 2);
-        l_run += sum;
         if (i + NSTAGE < c_n) issue(k + NSTAGE, c_lo + i + NSTAGE);
         // as in the MHA kernel: the next item is reserved shortly before this one ends
         if (threadIdx.x == 0 && i == max(c_n - 2, 0)) next = atomicAdd(&a.plan->work_counter, 1);
@@ -399,6 +432,10 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
       } else {
         fills = k0 + c_n;
       }
+#pragma unroll
+      for (int e = 0; e < NH; ++e)
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], m);
       if (wph > 1 && part > 0) {  // for the first warp of the head (this warp's stages are drained)
         float* xs = reinterpret_cast<float*>(my_stages);
 #pragma unroll
@@ -407,8 +444,11 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e) xs[((c * 2 + m) * 4 + e) * 32 + lane] = o[c][m][e];
-        xs[PIECES * 8 * 32 + lane] = ref;
-        xs[(PIECES * 8 + 1) * 32 + lane] = l_run;
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          xs[(PIECES * 8 + 2 * e) * 32 + lane] = ref[e];
+          xs[(PIECES * 8 + 2 * e + 1) * 32 + lane] = l_run[e];
+        }
         fence_proxy_async_shared();  // before the ring's next bulk copies into the same bytes
       }
     }
@@ -416,36 +456,35 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     if (mine && part == 0 && (wph > 1 ? !s_abort : ok)) {
       for (int other = 1; other < wph; ++other) {  // fold in the other warps' states
         const float* xs = reinterpret_cast<const float*>(my_stages + other * NSTAGE * Cfg::STAGE_BYTES);
-        const float rb = xs[PIECES * 8 * 32 + lane], lb = xs[(PIECES * 8 + 1) * 32 + lane];
-        const float M = fmaxf(ref, rb);
-        const float sa = ref == -INFINITY ? 0.f : exp2f(ref - M);
-        const float sb = rb == -INFINITY ? 0.f : exp2f(rb - M);
-        const float sa0 = __shfl_sync(kFullMask, sa, 8 * j), sa1 = __shfl_sync(kFullMask, sa, 8 * j + 4);
-        const float sb0 = __shfl_sync(kFullMask, sb, 8 * j), sb1 = __shfl_sync(kFullMask, sb, 8 * j + 4);
+        float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          const float rb = xs[(PIECES * 8 + 2 * e) * 32 + lane], lb = xs[(PIECES * 8 + 2 * e + 1) * 32 + lane];
+          const float M = fmaxf(ref[e], rb);
+          sa[e] = ref[e] == -INFINITY ? 0.f : exp2f(ref[e] - M);
+          sb[e] = rb == -INFINITY ? 0.f : exp2f(rb - M);
+          l_run[e] = l_run[e] * sa[e] + lb * sb[e];
+          ref[e] = M;
+        }
 #pragma unroll
         for (int c = 0; c < PIECES; ++c)
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[c][m][e] = o[c][m][e] * ((e & 1) ? sa1 : sa0) +
-                           xs[((c * 2 + m) * 4 + e) * 32 + lane] * ((e & 1) ? sb1 : sb0);
-        l_run = l_run * sa + lb * sb;
-        ref = M;
+              o[c][m][e] = o[c][m][e] * sa[e & 1] + xs[((c * 2 + m) * 4 + e) * 32 + lane] * sb[e & 1];
       }
       if (wph > 1) fence_proxy_async_shared();  // the other warps' rings are refilled after the loop's barrier
       // this lane holds dimensions 32 c + 4 r .. + 3 of heads 2 j and 2 j + 1
-      // the accumulators hold 2^-10 of their sums
-      const float inv = split ? 1024.f : ref != -INFINITY ? 1024.f / l_run : 0.f;
-      const float inv2[2] = {__shfl_sync(kFullMask, inv, 8 * j), __shfl_sync(kFullMask, inv, 8 * j + 4)};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < NH; ++e) {
         const int h = 2 * j + e;
         if (h >= G) continue;
+        // the accumulators hold 2^-10 of their sums
+        const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
 #pragma unroll
         for (int c = 0; c < PIECES; ++c) {
-          const float v[4] = {o[c][0][e] * inv2[e], o[c][0][2 + e] * inv2[e], o[c][1][e] * inv2[e],
-                              o[c][1][2 + e] * inv2[e]};
+          const float v[4] = {o[c][0][e] * inv, o[c][0][2 + e] * inv, o[c][1][e] * inv, o[c][1][2 + e] * inv};
           if (!split) {
             *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
                 make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
@@ -454,10 +493,10 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
                 make_float4(v[0], v[1], v[2], v[3]);
           }
         }
-      }
-      if (j == 0 && r < G) {
-        if (split) a.part_ml[(sh0 + r) * a.max_parts + p] = make_float2(ref, l_run);
-        else if (MASS) a.lse[sh0 + r] = ref + log2f(l_run);
+        if (r == 0) {
+          if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
+          else if (MASS) a.lse[sh0 + h] = ref[e] + log2f(l_run[e]);
+        }
       }
     }
     if (split) {

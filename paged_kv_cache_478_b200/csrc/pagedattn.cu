@@ -281,11 +281,12 @@ cudaError_t launch_gqa(const DecodeArgs& a, const DeviceState& dev, cudaStream_t
 template <typename T, int D>
 cudaError_t set_q4_attrs() {
   const int smem = (int)Q4Config<T, D>::smem_bytes(kMaxPartition);
-  const cudaError_t e = cudaFuncSetAttribute(paged_decode_q4_kernel<T, D, true>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_decode_q4_kernel<T, D, false>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaSuccess;
+  for (auto kernel : {paged_decode_q4_kernel<T, D, 1, false>, paged_decode_q4_kernel<T, D, 1, true>,
+                      paged_decode_q4_kernel<T, D, 2, false>, paged_decode_q4_kernel<T, D, 2, true>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e;
 }
 
 // Once per device, with that device current: resolve the error word's device
@@ -471,7 +472,10 @@ cudaError_t launch_decode(const DecodeArgs& a, const DeviceState& dev, cudaStrea
 template <typename T, int D>
 cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream, bool overlap) {
   using Cfg = Q4Config<T, D>;
-  auto kernel = a.scores ? paged_decode_q4_kernel<T, D, true> : paged_decode_q4_kernel<T, D, false>;
+  auto kernel = a.q_per_kv == 1 ? (a.scores ? paged_decode_q4_kernel<T, D, 1, true>
+                                            : paged_decode_q4_kernel<T, D, 1, false>)
+                                : (a.scores ? paged_decode_q4_kernel<T, D, 2, true>
+                                            : paged_decode_q4_kernel<T, D, 2, false>);
   const size_t smem = Cfg::smem_bytes(a.partition_size);
   int per_sm = 0;
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);

@@ -7,6 +7,7 @@
     python -m paged_kv_cache_478_b200.kernel_bench single-layer [--profile]
     python -m paged_kv_cache_478_b200.kernel_bench cache-ops [--profile]
     python -m paged_kv_cache_478_b200.kernel_bench decode-dtypes
+    python -m paged_kv_cache_478_b200.kernel_bench compress [--only NAME] [--profile]
 
 Each line printed is one JSON object.  These are the measurements behind the
 per-kernel tables of the design notes; the headline decode step is bench.py.
@@ -356,6 +357,116 @@ def decode_dtypes():
         del kp, vp
 
 
+def _q4_pool(nb, heads, dim, dtype, seed):
+    """K and V as 4-bit pools: N(0,1) values through pa_convert_blocks."""
+    code = {torch.float16: pa.PA_Q4_F16, torch.bfloat16: pa.PA_Q4_BF16}[dtype]
+    four = pa.pa_pool_create(nb, 16, heads, dim, code)
+    k4, v4 = (torch.empty((nb, heads, 9 * dim), dtype=torch.uint8, device="cuda") for _ in range(2))
+    step = 2048  # blocks converted at a time
+    wide = pa.pa_pool_create(step, 16, heads, dim, dtype)
+    kp = torch.empty((step, heads, 16, dim), dtype=dtype, device="cuda")
+    vp = torch.empty_like(kp)
+    for b in range(0, nb, step):
+        n = min(step, nb - b)
+        syn.fill_normal_device(kp, seed + 2 * b)
+        syn.fill_normal_device(vp, seed + 2 * b + 1)
+        at = torch.arange(n, dtype=torch.int32, device="cuda")
+        pa.pa_convert_blocks(wide, kp, vp, four, k4, v4, torch.stack([at, at + b], 1).contiguous())
+    return four, k4, v4
+
+
+def compress(only: str = "", partition_size: int = 0, profile: bool = False):
+    """4-bit pools (append, conversion, decode), decode with gathered weights, and eviction.  The
+    decode cases are one full-step layer, grouped queries (64 sequences, lengths uniform in [1,
+    2048], 8 KV heads x 8) and the long context; planned calls, device times."""
+    def report(name, fn, nbytes, **more):
+        if only and only != name:
+            return
+        if profile:
+            _profile_launches(fn, name)
+            return
+        us = _events_ms(fn, 50) * 1e3
+        _check()
+        print(json.dumps({"kernel": name, "us": round(us, 1), "GBps": round(nbytes / us / 1e3, 1), **more}), flush=True)
+
+    def wanted(*names):
+        return not only or only in names
+
+    decode = {"step": (syn.full_step_lengths(0, 200), 32, 1, torch.float16),
+              "gqa8": (syn.single_layer_lengths(0, 64), 8, 8, torch.bfloat16),
+              "long": (np.full(8, 32768, dtype=np.int32), 32, 1, torch.float16)}
+    D = 128
+    for case, (lens, H, G, dt) in decode.items():
+        if not wanted(f"decode4-{case}", f"decode4-mass-{case}", f"mass-{case}"):
+            continue
+        S, need = len(lens), [math.ceil(int(n) / 16) for n in lens]
+        nb, wide = sum(need), max(need)
+        tables = syn.random_tables(np.random.default_rng(0), lens, nb, wide)
+        bt, cl = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+        q = torch.randn((S, H * G, D), dtype=dt, device="cuda")
+        out, mass = torch.empty_like(q), torch.zeros((S, wide * 16), device="cuda")
+        for q4 in (True, False):
+            if q4:
+                pool, kp, vp = _q4_pool(nb, H, D, dt, 1)
+            elif wanted(f"mass-{case}"):
+                pool = pa.pa_pool_create(nb, 16, H, D, dt)
+                kp = torch.empty((nb, H, 16, D), dtype=dt, device="cuda")
+                vp = torch.empty_like(kp)
+                syn.fill_normal_device(kp, 1)
+                syn.fill_normal_device(vp, 2)
+            else:
+                continue
+            pa.pa_pool_set_query_heads(pool, H * G)
+            ws = torch.empty(pa.pa_decode_mass_workspace_bytes(pool, S, wide, 0, partition_size), dtype=torch.uint8, device="cuda")
+            pa.pa_decode_plan(pool, cl, wide, ws, partition_size=partition_size)
+            row = H * D * (9 / 16 if q4 else 2)
+            nbytes = 2 * int(lens.sum()) * row
+            if q4:
+                report(f"decode4-{case}", lambda: pa.pa_decode_attention_planned(
+                    pool, q, kp, vp, bt, 1 / math.sqrt(D), out, ws, partition_size=partition_size), nbytes,
+                       partition_size=partition_size or "auto")
+            report(f"decode4-mass-{case}" if q4 else f"mass-{case}", lambda: pa.pa_decode_attention_mass_planned(
+                pool, q, kp, vp, bt, 1 / math.sqrt(D), out, mass, mass, ws, decay=0.99, partition_size=partition_size),
+                   nbytes + 8 * int(lens.sum()), partition_size=partition_size or "auto")
+            del kp, vp
+    if wanted("append4", "convert-to-4", "convert-from-4"):
+        H, nb = 32, 1024
+        dt = torch.float16
+        four, k4, v4 = _q4_pool(nb, H, D, dt, 1)
+        wide = pa.pa_pool_create(nb, 16, H, D, dt)
+        kp = torch.randn((nb, H, 16, D), dtype=dt, device="cuda")
+        vp = torch.randn_like(kp)
+        pairs = torch.from_numpy(np.random.default_rng(0).permutation(nb).astype(np.int32)).cuda()
+        pairs = torch.stack([pairs, pairs.flip(0)], 1).contiguous()
+        kn, vn = torch.randn((nb * 16, H, D), dtype=dt, device="cuda"), torch.randn((nb * 16, H, D), dtype=dt, device="cuda")
+        slots = torch.arange(nb * 16, dtype=torch.int32, device="cuda")
+        nbytes = 2 * nb * 16 * H * D * (2 + 9 / 16)
+        report("append4", lambda: pa.pa_reshape_and_cache(four, kn, vn, slots, k4, v4), nbytes, tokens=nb * 16)
+        report("convert-to-4", lambda: pa.pa_convert_blocks(wide, kp, vp, four, k4, v4, pairs), nbytes, blocks=nb)
+        report("convert-from-4", lambda: pa.pa_convert_blocks(four, k4, v4, wide, kp, vp, pairs), nbytes, blocks=nb)
+    for name, S, L, keep in (("evict-200", 200, 2048, 1024), ("evict-long", 8, 32768, 8192)):
+        if not wanted(name):
+            continue
+        H, dt = 8, torch.float16
+        lens = np.linspace(1, L, S).astype(np.int32) if S > 8 else np.full(S, L, dtype=np.int32)
+        wide = L // 16
+        tables = np.random.default_rng(0).permutation(S * wide).astype(np.int32).reshape(S, wide)
+        pool = pa.pa_pool_create(S * wide, 16, H, D, dt)
+        kp = torch.randn((S * wide, H, 16, D), dtype=dt, device="cuda")
+        vp = torch.randn_like(kp)
+        track = dict(mass=torch.rand((S, L), device="cuda"), positions=torch.zeros((S, L), dtype=torch.int32, device="cuda"),
+                     history=torch.zeros((S, 2), dtype=torch.int32, device="cuda"))
+        after = {k: torch.zeros_like(v) for k, v in track.items()}
+        ws = torch.empty(pa.pa_evict_workspace_bytes(pool, S, wide), dtype=torch.uint8, device="cuda")
+        bt, cl = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+        keeps = torch.full((S,), keep, dtype=torch.int32, device="cuda")
+        call = lambda: pa.pa_evict_tokens(pool, kp, vp, bt, cl, keeps, 4, 128, track, after, ws)  # noqa: E731
+        call()
+        n = int((after["positions"][:, :keep] >= keep).sum())  # tokens moved
+        report(name, call, n * H * D * 2 * 4 + 16 * int(lens.sum()), moved_tokens=n)
+        del kp, vp
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     sub = ap.add_subparsers(dest="what", required=True)
@@ -378,6 +489,10 @@ def main(argv=None):
     p = sub.add_parser("cache-ops")
     p.add_argument("--profile", action="store_true")
     sub.add_parser("decode-dtypes")
+    p = sub.add_parser("compress")
+    p.add_argument("--only", default="", help="one of the printed kernel names")
+    p.add_argument("--partition-size", type=int, default=0, help="0 = automatic")
+    p.add_argument("--profile", action="store_true")
     args = ap.parse_args(argv)
     if not torch.cuda.is_available():
         raise SystemExit("kernel_bench needs a CUDA device")
@@ -395,6 +510,8 @@ def main(argv=None):
         single_layer(args.partition_size, args.profile)
     elif args.what == "cache-ops":
         cache_ops(args.profile)
+    elif args.what == "compress":
+        compress(args.only, args.partition_size, args.profile)
     else:
         decode_dtypes()
 

@@ -302,6 +302,25 @@ def test_nan_values_reach_their_own_group_only():
     assert torch.isnan(got[64:]).all() and torch.isfinite(got[:64]).all()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.125])
+def test_zero_and_negative_scales(scale):
+    c = dict(decode_case(13, [100, 17, 64], 2, 2, 64, "f16"), scale=scale)
+    want, _, _ = reference(c)
+    _, tol, _ = reference(dict(c, scale=abs(scale)))  # the same magnitudes
+    bound = oc.attend(c["qx"], oc.values(c["kp"], 64), oc.values(c["vp"], 64), c["lens"], c["tables"], scale)[2]
+    check(run_decode(c), want, np.maximum(tol, 2.0 ** -10 * bound + 2.0 ** -20))
+
+
+def test_a_nan_key_reaches_its_own_head_only():
+    c = decode_case(14, [70], 2, 1, 64, "bf16")
+    row = oc.values(c["kp"], 64)[c["tables"][0, 2], 1, 9].copy()
+    row[5] = np.inf
+    oc.store_row(c["kp"], c["tables"][0, 2], 1, 9, row)
+    for partition in (0, 16):
+        got = run_decode(c, partition)[0]
+        assert torch.isnan(got[1]).all() and torch.isfinite(got[0]).all()
+
+
 def test_bad_block_ids_are_reported():
     c = decode_case(8, [40, 20], 2, 1, 64, "f16")
     c["tables"][0, 1] = 10 ** 6
