@@ -49,6 +49,7 @@ template <typename T, int D>
 struct Q4Config {
   static constexpr int WARPS = 4;
   static constexpr int THREADS = WARPS * 32;
+  static constexpr int CTAS_PER_SM = 3;  // by registers (168) and shared memory (74 KB)
   static constexpr int TILE = q4_tile_bytes(D);
   static constexpr int HALF = kQ4ChunkBlocks * TILE;  // the K (or V) tiles of a stage
   static constexpr int STAGE_BYTES = 2 * HALF;

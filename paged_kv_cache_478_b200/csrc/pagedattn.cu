@@ -45,6 +45,7 @@ constexpr int kDecodeWarps = PA_DECODE_WARPS;    // heads per CTA (one warp each
 constexpr int kDecodeStages = PA_DECODE_STAGES;  // per-warp ring depth
 constexpr int kMinAutoPartition = 256;    // smallest partition the automatic choice makes
 constexpr int kFullBatchPartition = 512;  // partition when the batch alone fills the GPU
+constexpr int kLongPartition = 2048;      // longest automatic partition (4-bit pools)
 constexpr int kMaxPartition = 4096;
 
 struct DeviceState {
@@ -446,6 +447,27 @@ int auto_partition(int num_seqs, int head_groups, int max_context_len, int slots
   return std::max(kMinAutoPartition, round_up16(ps));
 }
 
+// Automatic partition size of the 4-bit kernel (slots: resident CTAs).  What an
+// item costs beside its tokens (plan entry, block table, first copies, partial
+// results and merge: about 6 us) weighs four times as much as on 16-bit pools,
+// so partitions are long where the batch allows it: about 3.6 times as many
+// tokens of the longest sequences as the slots, at most 2048 a partition
+// (200 requests x 32 heads up to 2048: 108 us at 2048, 120 at 512, 141 at 256;
+// 200 x 8 KV heads: 46 us at 512, 54 at 256 and at 768, 86 at 1536, where the
+// longest items outlast the rest; 8 x 32768 x 32 heads: 227 at 2048, 248 at 512).
+// A small batch gets one item per slot, the mean length taken as half the
+// longest, as long as that keeps partitions within 512 (64 x 8 KV heads up to
+// 2048: 34 us at 384, one item per slot; 41 at 256, 39 at 512).  Whole chunks.
+int auto_partition_q4(int num_seqs, int head_groups, int max_context_len, int slots) {
+  const int64_t tokens = (int64_t)num_seqs * head_groups * std::max(16, max_context_len);
+  // sequences of mean length m give about m / ps + 1 / 2 partitions each
+  const int64_t room = 2LL * slots - (int64_t)num_seqs * head_groups;
+  const int64_t single = room > 0 ? std::min<int64_t>(512, (tokens + room - 1) / room) : 512;
+  const int64_t ps = std::max<int64_t>(single, tokens * 5 / (18LL * slots));
+  const int64_t whole_chunks = (ps + kQ4Chunk - 1) / kQ4Chunk * kQ4Chunk;
+  return (int)std::min<int64_t>(kLongPartition, std::max<int64_t>(kMinAutoPartition, whole_chunks));
+}
+
 int resolve_max_context(const pa_pool* pool, int32_t max_blocks_per_seq, int32_t max_context_len) {
   const int64_t cap = (int64_t)max_blocks_per_seq * pool->block_size;
   const int64_t m = max_context_len == 0 ? cap : std::min<int64_t>(cap, max_context_len);
@@ -476,14 +498,10 @@ cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t 
                                             : paged_decode_q4_kernel<T, D, 1, false>)
                                 : (a.scores ? paged_decode_q4_kernel<T, D, 2, true>
                                             : paged_decode_q4_kernel<T, D, 2, false>);
-  const size_t smem = Cfg::smem_bytes(a.partition_size);
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Cfg::THREADS, smem);
-  if (e != cudaSuccess) return e;
-  per_sm = std::max(per_sm, 1);
   const int64_t upper = (int64_t)a.num_seqs * a.max_parts * a.head_groups;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(upper, (int64_t)dev.num_sms * per_sm));
-  return launch_decode_grid(kernel, grid, Cfg::THREADS, smem, stream, a, overlap, q4_heads_per_item(a.heads));
+  const int grid = (int)std::min<int64_t>(upper, (int64_t)dev.num_sms * Cfg::CTAS_PER_SM);
+  return launch_decode_grid(kernel, grid, Cfg::THREADS, Cfg::smem_bytes(a.partition_size), stream, a,
+                            overlap, q4_heads_per_item(a.heads));
 }
 
 template <typename T, int D>
@@ -680,6 +698,8 @@ pa_status prepare_decode(const pa_pool* pool, int32_t num_seqs, int32_t max_bloc
   const int ps = partition_size != 0 ? partition_size
                  : max_shared_blocks > 0
                      ? kMinAutoPartition
+                 : is_q4(pool) ? auto_partition_q4(num_seqs, head_groups, maxL,
+                                                   (*dev)->num_sms * Q4Config<__half, 128>::CTAS_PER_SM)
                      : auto_partition(num_seqs, head_groups, maxL,
                                       (*dev)->num_sms * (*dev)->decode_ctas_per_sm,
                                       use_gqa_mma(pool) ? 1 : 2);

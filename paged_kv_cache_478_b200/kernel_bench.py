@@ -378,7 +378,8 @@ def _q4_pool(nb, heads, dim, dtype, seed):
 def compress(only: str = "", partition_size: int = 0, profile: bool = False):
     """4-bit pools (append, conversion, decode), decode with gathered weights, and eviction.  The
     decode cases are one full-step layer, grouped queries (64 sequences, lengths uniform in [1,
-    2048], 8 KV heads x 8) and the long context; planned calls, device times."""
+    2048], 8 KV heads x 8; the full step's 200, 8 x 4) and the long context; planned calls, device
+    times."""
     def report(name, fn, nbytes, **more):
         if only and only != name:
             return
@@ -394,6 +395,7 @@ def compress(only: str = "", partition_size: int = 0, profile: bool = False):
 
     decode = {"step": (syn.full_step_lengths(0, 200), 32, 1, torch.float16),
               "gqa8": (syn.single_layer_lengths(0, 64), 8, 8, torch.bfloat16),
+              "gqa4": (syn.full_step_lengths(0, 200), 8, 4, torch.bfloat16),
               "long": (np.full(8, 32768, dtype=np.int32), 32, 1, torch.float16)}
     D = 128
     for case, (lens, H, G, dt) in decode.items():
