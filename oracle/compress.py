@@ -32,7 +32,7 @@ def quantise(x):
     bad = ~np.isfinite(g).all(-1) | ~np.isfinite(s) | ((hi - lo) > np.finfo(np.float32).max)
     flat = (s == 0) | bad
     d = np.where(flat, 1.0, s)
-    z = np.where(flat, 0.0, np.rint(-np.where(flat, 0.0, lo) / d))
+    z = np.where(flat, 0.0, np.rint(-np.where(flat, 0.0, lo) / d)) + 0.0  # no negative zero
     n = np.clip(np.rint(np.where(flat[..., None], 0.0, g) / d[..., None]) + z[..., None], 0, 15)
     return n.reshape(x.shape).astype(np.uint8), np.where(bad, np.nan, s), z
 

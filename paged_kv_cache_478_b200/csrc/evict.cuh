@@ -13,8 +13,14 @@
 // The track of a sequence: mass[t], positions[t] (the original position of
 // the token in slot t, for t < held) and history = (held, next): slots at or
 // past `held` arrived since, in order, from position `next` on.
+// Selecting is a radix selection of the keep-th key, 11 bits a pass.  A cluster
+// of up to 8 CTAs takes a sequence, each a contiguous share of its slots, with the
+// keys in shared memory: the track is read once, the passes add their
+// histograms over distributed shared memory.  Moving is bound by memory: rows of
+// one token and head (256 bytes at head_dim 128 in 16 bits) read and written once.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -36,16 +42,20 @@ struct EvictArgs {
   int32_t* positions_out;
   int32_t* history_out;
   int64_t in_stride, out_stride;
-  int32_t* counts;  // [S] moves of each sequence
-  int2* moves;      // [S][move_cap] (source, destination), physical slots
+  int4* heads;   // [S] number of moves, then the sequence's history before
+  int2* moves;   // [S][move_cap] (source, destination) slots of the sequence
   uint32_t* err;
   int64_t num_blocks;
   int32_t max_blocks_per_seq;
-  int32_t num_seqs;
   int32_t max_context_len;
   int32_t move_cap;
   int32_t sinks, recent;
 };
+
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictMaxCluster = 8;
+constexpr int kEvictCachedKeys = 40 * 1024;  // of one CTA, 160 KB; longer shares are read anew each pass
 
 // Order of eviction as an unsigned number: mass ascending, NaN above
 // infinity, protected tokens above all.
@@ -81,167 +91,265 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// One CTA per sequence: a radix selection of the keep-th key, 8 bits a pass,
-// then the moves and the new track.
-__global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int s = blockIdx.x, tid = threadIdx.x;
+struct EvictShared {
+  int hist[kEvictBins];
+  int warp_sums[32];
+  uint32_t prefix;
+  int need;
+  int ties, holes, movers;  // of this CTA's share
+};
+
+// One cluster per sequence.  CACHED: the CTA's keys are held in the dynamic
+// shared memory.
+template <bool CACHED>
+__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a) {
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t evict_keys[];
+  __shared__ EvictShared sh;
+  grid_dependents_launch();  // the moving kernel may start its CTAs; they wait for this grid
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int s = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t cap = min((int64_t)a.max_context_len, (int64_t)a.max_blocks_per_seq * kBlock);
   int L = a.context_lens[s];
-  if (L < 0 || L > cap) {
-    if (tid == 0) atomicOr(a.err, PA_DEVERR_CONTEXT_LEN);
-    L = L < 0 ? 0 : (int)cap;
-  }
   int keep = a.keep_lens[s];
-  if (keep < 0) {
-    if (tid == 0) atomicOr(a.err, PA_DEVERR_CONTEXT_LEN);
-    keep = L;
-  }
+  if (rank == 0 && tid == 0 && (L < 0 || L > cap || keep < 0)) atomicOr(a.err, PA_DEVERR_CONTEXT_LEN);
+  L = L < 0 ? 0 : L > cap ? (int)cap : L;
+  if (keep < 0) keep = L;
   const float* mass = a.mass_in + s * a.in_stride;
   const int32_t* pos = a.positions_in + s * a.in_stride;
   float* mass_out = a.mass_out + s * a.out_stride;
   int32_t* pos_out = a.positions_out + s * a.out_stride;
   const int held = a.history_in[2 * s], next = a.history_in[2 * s + 1];
+  cluster.sync();  // every CTA of the cluster has read the history before one writes it in place
+  // this CTA's slots, each warp's of them contiguous and a multiple of 32
+  const int per = (L + C * kEvictThreads - 1) / (C * kEvictThreads) * kEvictThreads;
+  const int lo = min(L, rank * per), hi = min(L, lo + per);
   if (keep >= L) {  // nothing to evict
-    if (tid == 0) {
-      a.counts[s] = 0;
+    if (rank == 0 && tid == 0) {
+      a.heads[s] = make_int4(0, held, next, 0);
       a.history_out[2 * s] = held;
       a.history_out[2 * s + 1] = next;
     }
     if (mass_out != mass)
-      for (int t = tid; t < L; t += 1024) mass_out[t] = mass[t];
+      for (int t = lo + tid; t < hi; t += kEvictThreads) mass_out[t] = mass[t];
     if (pos_out != pos)
-      for (int t = tid; t < L; t += 1024) pos_out[t] = pos[t];
-    return;
+      for (int t = lo + tid; t < hi; t += kEvictThreads) pos_out[t] = pos[t];
+    return;  // the same in every CTA of the cluster
   }
   const int seen = next + L - held;
   auto position = [&](int t) { return t < held ? pos[t] : next + t - held; };
-  auto key = [&](int t) {
+  auto make_key = [&](int t) {
     const int at = position(t);
     return at < a.sinks || at >= seen - a.recent ? 0xffffffffu : evict_key(mass[t]);
   };
-  // the keep-th largest key, and how many tokens of that key stay
+  auto key = [&](int t) { return CACHED ? evict_keys[t - lo] : make_key(t); };
+  if (CACHED)
+    for (int t = lo + tid; t < hi; t += kEvictThreads) evict_keys[t - lo] = make_key(t);
   if (tid == 0) {
-    s_prefix = 0;
-    s_need = keep;
+    sh.prefix = 0;
+    sh.need = keep;
   }
-  for (int shift = 24; shift >= 0 && keep > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += 1024) hist[i] = 0;
+  // the keep-th largest key (sh.prefix), and how many tokens of that key stay (sh.need)
+  for (int pass = 0; pass < 3 && keep > 0; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
     __syncthreads();
-    const uint32_t prefix = s_prefix;
-    for (int t = tid; t < L; t += 1024) {
+    const uint32_t prefix = sh.prefix;
+    const int need = sh.need;
+    for (int t = lo + tid; t < hi; t += kEvictThreads) {
       const uint32_t k = key(t);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&sh.hist[(k >> shift) & digit], 1);
     }
-    __syncthreads();
-    if (tid == 0) {
-      int need = s_need, b = 255;
-      while (b > 0 && hist[b] < need) need -= hist[b--];
-      s_prefix = (prefix << 8) | (uint32_t)b;
-      s_need = need;
+    cluster.sync();
+    // two bins a thread, the largest first, summed over the cluster
+    int n[2] = {0, 0};
+    for (int c = 0; c < C; ++c) {
+      const int* h = cluster.map_shared_rank(sh.hist, c);
+      n[0] += h[kEvictBins - 1 - 2 * tid];
+      n[1] += h[kEvictBins - 2 - 2 * tid];
     }
-    __syncthreads();
+    int total;
+    const int above = block_scan(n[0] + n[1], sh.warp_sums, &total);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int before = above + (e ? n[0] : 0);
+      if (before < need && need <= before + n[e]) {  // one thread of the block
+        sh.prefix = (prefix << (pass == 2 ? 10 : 11)) | (uint32_t)(kEvictBins - 1 - 2 * tid - e);
+        sh.need = need - before;
+      }
+    }
+    cluster.sync();  // the histograms are free again
   }
-  __syncthreads();
-  const uint32_t edge = s_prefix;
-  const int ties = s_need;  // of the tokens at the edge, the first this many stay
+  const uint32_t edge = sh.prefix;
+  const int ties = sh.need;  // of the tokens at the edge, the first this many stay
+
+  // Sums before this CTA over the cluster's shares, of a member of its shared memory.
+  auto before = [&](int EvictShared::* member, int* total) {
+    int sum = 0, all = 0;
+    for (int c = 0; c < C; ++c) {
+      const int v = cluster.map_shared_rank(&sh, c)->*member;
+      sum += c < rank ? v : 0;
+      all += v;
+    }
+    if (total) *total = all;
+    return sum;
+  };
+  const int wlo = lo + warp * (per / 32), whi = min(hi, wlo + per / 32);
+  // sweep 1: tokens at the edge
+  int count = 0, total;
+  for (int t0 = wlo; t0 < whi; t0 += 32) {
+    const int t = t0 + lane;
+    count += __popc(__ballot_sync(kFullMask, t < whi && keep > 0 && key(t) == edge));
+  }
+  int rank_of_warp = block_scan(lane == 0 ? count : 0, sh.warp_sums, &total);
+  rank_of_warp = __shfl_sync(kFullMask, rank_of_warp, 0);
+  if (tid == 0) sh.ties = total;
+  cluster.sync();
+  const int tie0 = before(&EvictShared::ties, nullptr) + rank_of_warp;
+  // Who stays in the 32 slots from t0 on; tie: rank of the first token at the edge.
+  auto stays_of = [&](int t0, int& tie) {
+    const int t = t0 + lane;
+    const uint32_t k = t < whi && keep > 0 ? key(t) : 0u;
+    const bool at_edge = t < whi && keep > 0 && k == edge;
+    const uint32_t edges = __ballot_sync(kFullMask, at_edge);
+    const bool stays = t < whi && keep > 0 &&
+                       (k > edge || (at_edge && tie + __popc(edges & ((1u << lane) - 1u)) < ties));
+    tie += __popc(edges);
+    return stays;
+  };
+  // sweep 2: holes and movers of every warp
+  int holes = 0, movers = 0, tie = tie0;
+  for (int t0 = wlo; t0 < whi; t0 += 32) {
+    const int t = t0 + lane;
+    const bool stays = stays_of(t0, tie);
+    holes += __popc(__ballot_sync(kFullMask, t < whi && t < keep && !stays));
+    movers += __popc(__ballot_sync(kFullMask, t >= keep && stays));
+  }
+  int hole = block_scan(lane == 0 ? holes : 0, sh.warp_sums, &total);
+  if (tid == 0) sh.holes = total;
+  int mover = block_scan(lane == 0 ? movers : 0, sh.warp_sums, &total);
+  if (tid == 0) sh.movers = total;
+  cluster.sync();
+  int all_movers;
+  hole = before(&EvictShared::holes, nullptr) + __shfl_sync(kFullMask, hole, 0);
+  mover = before(&EvictShared::movers, &all_movers) + __shfl_sync(kFullMask, mover, 0);
+  // sweep 3: the moves, and the track of what is not moved
   int2* moves = a.moves + (int64_t)s * a.move_cap;
-  int done_ties = 0, holes = 0, movers = 0;
-  for (int t0 = 0; t0 < L; t0 += 1024) {
-    const int t = t0 + tid;
-    const uint32_t k = t < L ? key(t) : 0u;
-    const bool tie = t < L && keep > 0 && k == edge;
-    int n;
-    const int rank = done_ties + block_scan(tie, warp_sums, &n);
-    done_ties += n;
-    const bool stays = t < L && keep > 0 && (k > edge || (tie && rank < ties));
-    const bool hole = t < keep && !stays, mover = t >= keep && stays;
-    const int hi = holes + block_scan(hole, warp_sums, &n);
-    holes += n;
-    const int mi = movers + block_scan(mover, warp_sums, &n);
-    movers += n;
-    if (hole) moves[hi].y = t;
-    if (mover) moves[mi].x = t;
+  tie = tie0;
+  for (int t0 = wlo; t0 < whi; t0 += 32) {
+    const int t = t0 + lane;
+    const bool stays = stays_of(t0, tie);
+    const bool is_hole = t < whi && t < keep && !stays, is_mover = t >= keep && stays;
+    const uint32_t hb = __ballot_sync(kFullMask, is_hole), mb = __ballot_sync(kFullMask, is_mover);
+    const uint32_t below = (1u << lane) - 1u;
+    if (is_hole) moves[hole + __popc(hb & below)].y = t;
+    if (is_mover) moves[mover + __popc(mb & below)].x = t;
+    hole += __popc(hb);
+    mover += __popc(mb);
     if (t < keep && stays) {
       const int at = position(t);
       if (mass_out != mass) mass_out[t] = mass[t];
       pos_out[t] = at;
+    } else if (t < whi && t >= keep && !stays) {
+      mass_out[t] = 0.f;
     }
   }
-  __syncthreads();
-  const int32_t* table = a.block_tables + (int64_t)s * a.max_blocks_per_seq;
-  auto physical = [&](int t) {
-    int32_t b = table[t / kBlock];
-    if (b < 0 || b >= a.num_blocks) {
-      atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-      return -1;
-    }
-    return b * kBlock + t % kBlock;
-  };
-  for (int i = tid; i < movers; i += 1024) {
-    const int2 mv = moves[i];
-    mass_out[mv.y] = mass[mv.x];
-    pos_out[mv.y] = position(mv.x);
-    moves[i] = make_int2(physical(mv.x), physical(mv.y));
-  }
-  __syncthreads();
-  for (int t = keep + tid; t < L; t += 1024) mass_out[t] = 0.f;
-  if (tid == 0) {
-    a.counts[s] = movers;
+  if (rank == 0 && tid == 0) {
+    a.heads[s] = make_int4(all_movers, held, next, 0);
     a.history_out[2 * s] = keep;
     a.history_out[2 * s + 1] = seen;
   }
+  cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
-// Move the K and V rows of every listed token: one thread per 16-byte chunk
-// (4-byte word of a 4-bit pool), heads innermost but one.
-// row_chunks: 16-byte chunks per row of a head.
-__global__ void __launch_bounds__(256)
-    evict_move_kernel(EvictArgs a, uint4* __restrict__ k_pool, uint4* __restrict__ v_pool, int heads,
-                      int row_chunks) {
-  const int s = blockIdx.y;
-  const int n = a.counts[s];
-  const int64_t per = (int64_t)heads * row_chunks, total = n * per;
-  const int2* moves = a.moves + (int64_t)s * a.move_cap;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per;
-    const int rest = (int)(i - m * per);
-    const int h = rest / row_chunks, c = rest - h * row_chunks;
-    const int2 mv = moves[m];
-    if (mv.x < 0 || mv.y < 0) continue;  // a bad block id, reported
-    const int64_t src = (((int64_t)(mv.x >> 4) * heads + h) * 16 + (mv.x & 15)) * row_chunks + c;
-    const int64_t dst = (((int64_t)(mv.y >> 4) * heads + h) * 16 + (mv.y & 15)) * row_chunks + c;
-    k_pool[dst] = k_pool[src];
-    v_pool[dst] = v_pool[src];
-  }
-}
+constexpr int kEvictMovesPerCta = 16;
 
-// The same for 4-bit pools: D / 8 data words and D / 64 group words a row.
+// Move the K and V rows of the listed tokens and their tracks.  `units` 16-byte
+// copies make a head's row; 4-bit rows have their group words beside them.
+template <bool Q4>
 __global__ void __launch_bounds__(256)
-    evict_move_q4_kernel(EvictArgs a, uint8_t* __restrict__ k_pool, uint8_t* __restrict__ v_pool,
-                         int heads, int D) {
+    evict_move_kernel(EvictArgs a, uint8_t* __restrict__ k_pool, uint8_t* __restrict__ v_pool, int heads,
+                      int D, int units) {
+  __shared__ int2 slots[kEvictMovesPerCta];  // physical, -1: a bad block id
+  grid_dependency_wait();  // the selecting kernel
   const int s = blockIdx.y;
-  const int n = a.counts[s];
-  const int data = D / 8, words = data + D / 64;
-  const int64_t per = (int64_t)heads * words, total = n * per;
-  const int2* moves = a.moves + (int64_t)s * a.move_cap;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per;
-    const int rest = (int)(i - m * per);
-    const int h = rest / words, c = rest - h * words;
-    const int2 mv = moves[m];
-    if (mv.x < 0 || mv.y < 0) continue;
-    auto at = [&](int slot) {
-      const int64_t tile = ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D);
-      return tile + (c < data ? (c / 4) * 256 + (slot & 15) * 16 + (c % 4) * 4
-                              : q4_words_off(D) + ((c - data) * 16 + (slot & 15)) * 4);
+  const int4 head = a.heads[s];
+  const int32_t* table = a.block_tables + (int64_t)s * a.max_blocks_per_seq;
+  for (int m0 = blockIdx.x * kEvictMovesPerCta; m0 < head.x; m0 += gridDim.x * kEvictMovesPerCta) {
+    const int n = min(kEvictMovesPerCta, head.x - m0);
+    __syncthreads();  // slots are free again
+    if (threadIdx.x < 2 * n) {
+      const int2 mv = a.moves[(int64_t)s * a.move_cap + m0 + threadIdx.x / 2];
+      const int t = (threadIdx.x & 1) ? mv.y : mv.x;
+      int32_t b = table[t / kBlock];
+      if (b < 0 || b >= a.num_blocks) {
+        atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+        b = -1;
+      }
+      reinterpret_cast<int*>(slots)[threadIdx.x] = b < 0 ? -1 : b * kBlock + t % kBlock;
+      if ((threadIdx.x & 1) == 0) {  // the token's track; its old slot starts from 0 again
+        const int64_t in = s * a.in_stride + mv.x, out = s * a.out_stride;
+        const float mass = a.mass_in[in];
+        const int at = mv.x < head.y ? a.positions_in[in] : head.z + mv.x - head.y;
+        a.mass_out[out + mv.y] = mass;
+        a.positions_out[out + mv.y] = at;
+        a.mass_out[out + mv.x] = 0.f;
+      }
+    }
+    __syncthreads();
+    const int per = heads * units, total = n * per;
+    // (in-block row, 16-byte units) of a slot's row of a head
+    auto at = [&](int slot, int h, int c) {
+      if constexpr (Q4)
+        return ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D) + c * 256 + (slot & 15) * 16;
+      else
+        return ((((int64_t)(slot >> 4) * heads + h) * 16 + (slot & 15)) * units + c) * 16;
     };
-    const int64_t src = at(mv.x), dst = at(mv.y);
-    *reinterpret_cast<uint32_t*>(k_pool + dst) = *reinterpret_cast<const uint32_t*>(k_pool + src);
-    *reinterpret_cast<uint32_t*>(v_pool + dst) = *reinterpret_cast<const uint32_t*>(v_pool + src);
+    constexpr int U = 4;  // copies of K and of V in flight in a thread
+    for (int i0 = threadIdx.x; i0 < total; i0 += U * 256) {
+      uint4 kv[U][2];
+      int64_t to[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * 256;
+        to[u] = -1;
+        if (i < total) {
+          const int m = i / per, rest = i - m * per, h = rest / units, c = rest - h * units;
+          const int2 mv = slots[m];
+          if (mv.x >= 0 && mv.y >= 0) {
+            const int64_t from = at(mv.x, h, c);
+            to[u] = at(mv.y, h, c);
+            kv[u][0] = *reinterpret_cast<const uint4*>(k_pool + from);
+            kv[u][1] = *reinterpret_cast<const uint4*>(v_pool + from);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (to[u] >= 0) {
+          *reinterpret_cast<uint4*>(k_pool + to[u]) = kv[u][0];
+          *reinterpret_cast<uint4*>(v_pool + to[u]) = kv[u][1];
+        }
+    }
+    if constexpr (Q4) {  // the group words
+      const int groups = D / 64, words = heads * groups;
+      for (int i = threadIdx.x; i < n * words; i += 256) {
+        const int m = i / words, rest = i - m * words, h = rest / groups, g = rest - h * groups;
+        const int2 mv = slots[m];
+        if (mv.x < 0 || mv.y < 0) continue;
+        auto word = [&](int slot) {
+          return ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D) + q4_words_off(D) +
+                 (g * 16 + (slot & 15)) * 4;
+        };
+        const int64_t from = word(mv.x), dst = word(mv.y);
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(k_pool + from);
+        const uint32_t vw = *reinterpret_cast<const uint32_t*>(v_pool + from);
+        *reinterpret_cast<uint32_t*>(k_pool + dst) = kw;
+        *reinterpret_cast<uint32_t*>(v_pool + dst) = vw;
+      }
+    }
   }
 }
 

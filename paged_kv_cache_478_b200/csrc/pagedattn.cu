@@ -263,6 +263,46 @@ cudaError_t launch_decode_grid(K kernel, int grid, int threads, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kernel, a, extra...);
 }
 
+// Launch a kernel as a programmatic dependent of the preceding one of its
+// stream: it waits for that one itself (grid_dependency_wait).
+template <typename K, typename... Args>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The selection of pa_evict_tokens: a cluster per sequence, sized for 4096 keys
+// a CTA (8 x 32768 tokens: %SEL8% us with 8 CTAs a sequence, %SEL1% with one; 200
+// x 2048: one CTA each).
+cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, cudaStream_t stream) {
+  int cluster = 1;
+  while (cluster < kEvictMaxCluster && a.max_context_len > cluster * 4096) cluster *= 2;
+  const int64_t rounds = ((int64_t)a.max_context_len + cluster * kEvictThreads - 1) / (cluster * kEvictThreads);
+  const int64_t keys = std::max<int64_t>(1, rounds) * kEvictThreads;  // of one CTA
+  const bool cached = keys <= kEvictCachedKeys;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(num_seqs * cluster));
+  cfg.blockDim = dim3((unsigned)kEvictThreads);
+  cfg.dynamicSmemBytes = cached ? (size_t)keys * 4 : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cached ? evict_select_kernel<true> : evict_select_kernel<false>, a);
+}
+
 template <typename T, int D>
 cudaError_t launch_gqa(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream,
                        const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool overlap = false) {
@@ -323,6 +363,9 @@ pa_status device_state(DeviceState** out) {
                            set_gqa_attrs<__half, 128>(),
                            set_gqa_attrs<__nv_bfloat16, 64>(),
                            set_gqa_attrs<__nv_bfloat16, 128>(),
+                           cudaFuncSetAttribute(evict_select_kernel<true>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                kEvictCachedKeys * 4),
                            set_q4_attrs<__half, 64>(),
                            set_q4_attrs<__half, 128>(),
                            set_q4_attrs<__nv_bfloat16, 64>(),
@@ -1298,14 +1341,14 @@ pa_status decode_mass(const pa_pool* pool, const void* q, const void* k_pool, co
 }
 
 struct EvictLayout {
-  size_t counts = 0, moves = 0, total = 0;
+  size_t heads = 0, moves = 0, total = 0;
   int64_t cap = 0;  // moves of one sequence: at most half of its tokens
 };
 
 EvictLayout evict_layout(int64_t S, int maxL) {
   EvictLayout e;
   e.cap = std::max(1, maxL / 2);
-  e.moves = align256(S * 4);
+  e.moves = align256(S * sizeof(int4));
   e.total = align256(e.moves + S * e.cap * 8);
   return e;
 }
@@ -1393,31 +1436,27 @@ pa_status pa_evict_tokens(const pa_pool* pool, void* k_pool, void* v_pool,
   a.history_out = out->history;
   a.in_stride = in->stride;
   a.out_stride = out->stride;
-  a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + w.counts);
+  a.heads = reinterpret_cast<int4*>(static_cast<char*>(workspace) + w.heads);
   a.moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) + w.moves);
   a.err = dev->err;
   a.num_blocks = pool->num_blocks;
   a.max_blocks_per_seq = max_blocks_per_seq;
-  a.num_seqs = num_seqs;
   a.max_context_len = maxL;
   a.move_cap = (int32_t)w.cap;
   a.sinks = sinks;
   a.recent = recent;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<num_seqs, 1024, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_evict_select(a, num_seqs, s);
   if (e != cudaSuccess) return cuda_fail(e, "evict select launch");
-  // the number of moves is known on the device only: enough CTAs to fill the GPU
-  const int64_t chunks = w.cap * block_bytes(pool) / kBlock / (is_q4(pool) ? 4 : 16);
-  const int64_t want = std::max<int64_t>(1, (int64_t)dev->num_sms * 8 / num_seqs);
-  const dim3 grid((unsigned)std::min<int64_t>((chunks + 255) / 256, want), (unsigned)num_seqs);
-  if (is_q4(pool))
-    evict_move_q4_kernel<<<grid, 256, 0, s>>>(a, static_cast<uint8_t*>(k_pool),
-                                              static_cast<uint8_t*>(v_pool), pool->heads, pool->head_dim);
-  else
-    evict_move_kernel<<<grid, 256, 0, s>>>(a, static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool),
-                                           pool->heads, pool->head_dim * pool->elem_bytes / 16);
-  e = cudaGetLastError();
+  if (maxL < 2) return PA_OK;  // one slot: nothing can move
+  // CTAs past a sequence's moves (known on the device only) leave at once
+  const bool q4 = is_q4(pool);
+  const int units = q4 ? pool->head_dim / 32 : pool->head_dim * pool->elem_bytes / 16;
+  const int64_t ctas = (w.cap + kEvictMovesPerCta - 1) / kEvictMovesPerCta;
+  const dim3 grid((unsigned)std::min<int64_t>(ctas, 4096), (unsigned)num_seqs);
+  e = launch_dependent(q4 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 256, s, a,
+                       static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), pool->heads,
+                       pool->head_dim, units);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "evict move launch");
 }
 

@@ -17,10 +17,8 @@
 // z may lie outside 0..15, so a group far from zero keeps the full
 // resolution of its range; the second term of s keeps |z| below 2048, where
 // fp16 holds every whole number.  The error is at most s / 2, and a few
-// hundredths of s more at the upper end where s was rounded down.  x / s has
-// a quotient of at most 11 by 8 significant bits, which is never so near to a
-// half without being one that fp32 division would round it there: n and z are
-// those of exact arithmetic.  A group that holds an infinity or NaN, or whose
+// hundredths of s more at the upper end where s was rounded down.  n and z are
+// those of exact quotients (q4_quotient).  A group that holds an infinity or NaN, or whose
 // range passes fp32, gets s = NaN and reads back as NaN.
 #pragma once
 
@@ -44,28 +42,63 @@ __device__ __forceinline__ float q4_zero(uint32_t word) {
   return __half2float(__ushort_as_half((unsigned short)(word & 0xffffu)));
 }
 
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+  using V = __half2;
+  __device__ __forceinline__ static V max_nan(V a, V b) { return __hmax2_nan(a, b); }
+  __device__ __forceinline__ static V min_nan(V a, V b) { return __hmin2_nan(a, b); }
+  __device__ __forceinline__ static float2 floats(V a) { return __half22float2(a); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  __device__ __forceinline__ static V max_nan(V a, V b) { return __hmax2_nan(a, b); }
+  __device__ __forceinline__ static V min_nan(V a, V b) { return __hmin2_nan(a, b); }
+  __device__ __forceinline__ static float2 floats(V a) { return __bfloat1622float2(a); }
+};
+
+constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: x + kRoundMagic holds round(x) in its low bits
+
+// round(x / s) + kRoundMagic, given inv = 1 / s rounded, halves to even as
+// the exact quotient has them.  x * inv is off by at most 2^-23 of itself.  A
+// quotient of 11 by 8 significant bits below 2048 that is no half differs from
+// one by 2^-9 or by 2^-12 of itself, at any rate by 2^-20 of itself: rounding x *
+// inv to 21 bits (Veltkamp's splitting, by at most 2^-21) puts halves back on
+// their place and moves nothing onto or across one.
+__device__ __forceinline__ float q4_quotient(float x, float inv) {
+  const float q = __fmul_rn(x, inv);
+  const float c = __fmul_rn(q, 9.f);
+  const float h = __fsub_rn(c, __fsub_rn(c, q));
+  return __fadd_rn(h, kRoundMagic);
+}
+
 // Quantise one group of 64 values held by 8 neighbouring lanes, 8 each (all
 // 32 lanes of the warp call).  Returns the lane's 8 numbers, the first in the
-// lowest 4 bits; *word is the group's word.
-__device__ __forceinline__ uint32_t q4_quantise(const float* x, int lane, uint32_t* word) {
-  float hi = x[0], lo = x[0], probe = 0.f;
+// lowest 4 bits; *word is the group's word.  The largest and smallest value are
+// found in the 16-bit type, NaN winning, as one pair (max, -min) across the
+// lanes.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_quantise(const uint4& u, uint32_t* word) {
+  using P = Pair<T>;
+  using V = typename P::V;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  auto as_v = [](uint32_t x) { return *reinterpret_cast<const V*>(&x); };
+  auto as_u = [](V x) { return *reinterpret_cast<uint32_t*>(&x); };
+  const V m = P::max_nan(P::max_nan(as_v(w[0]), as_v(w[1])), P::max_nan(as_v(w[2]), as_v(w[3])));
+  const V l = P::min_nan(P::min_nan(as_v(w[0]), as_v(w[1])), P::min_nan(as_v(w[2]), as_v(w[3])));
+  const uint32_t mu = as_u(m), lu = as_u(l) ^ 0x80008000u;
+  V top = P::max_nan(as_v(__byte_perm(mu, lu, 0x5410)), as_v(__byte_perm(mu, lu, 0x7632)));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    hi = fmaxf(hi, x[e]);
-    lo = fminf(lo, x[e]);
-    probe = fmaf(x[e], 0.f, probe);  // NaN once any value is an infinity or NaN
-  }
-  const uint32_t bad = __ballot_sync(kFullMask, probe != 0.f);
-#pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-    hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, m));
-    lo = fminf(lo, __shfl_xor_sync(kFullMask, lo, m));
-  }
-  const float range = __fsub_rn(hi, lo);
-  const float top = fmaxf(fabsf(hi), fabsf(lo));
-  const float raw = fmaxf(__fdiv_rn(range, 15.f), __fdiv_rn(top, 2000.f));
+  for (int k = 1; k < 8; k <<= 1) top = P::max_nan(top, as_v(__shfl_xor_sync(kFullMask, as_u(top), k)));
+  const float2 ends = P::floats(top);
+  const float hi = ends.x, lo = -ends.y;
+  float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
+  const float big = fmaxf(fabsf(hi), fabsf(lo));
+  if (big > 1990.f * raw) raw = fmaxf(raw, __fdiv_rn(big, 2000.f));  // the other quotient may be the larger
   const float s = __bfloat162float(__float2bfloat16_rn(raw));
-  if (((bad >> (lane & 24)) & 0xffu) != 0u || !(s < INFINITY)) {
+  if (!(s < INFINITY)) {
     *word = 0x7fc00000u;  // s = NaN, z = 0
     return 0u;
   }
@@ -73,13 +106,25 @@ __device__ __forceinline__ uint32_t q4_quantise(const float* x, int lane, uint32
     *word = 0u;
     return 0u;
   }
-  const float z = rintf(__fdiv_rn(-lo, s));
+  float x[8];
+  Chunk<T>::to_float(u, x);
   uint32_t n = 0;
+  if (s < 1e-36f) {  // 1 / s or a product may leave the normal numbers: divide
+    const float z = rintf(__fdiv_rn(-lo, s)) + 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + z, 0.f), 15.f);
-    n |= (uint32_t)v << (4 * e);
+    for (int e = 0; e < 8; ++e) {
+      const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + z, 0.f), 15.f);
+      n |= (uint32_t)v << (4 * e);
+    }
+    *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
+    return n;
   }
+  const float inv = __frcp_rn(s);
+  const float z = __fsub_rn(q4_quotient(-lo, inv), kRoundMagic);
+  const int off = (int)z - __float_as_int(kRoundMagic);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)  // clamp(round(x / s) + z, 0, 15)
+    n += (uint32_t)__viaddmin_s32_relu(__float_as_int(q4_quotient(x[e], inv)), off, 15) << (4 * e);
   *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
   return n;
 }
@@ -120,12 +165,9 @@ __global__ void __launch_bounds__(256)
       ku = *reinterpret_cast<const uint4*>(k_new + src);
       vu = *reinterpret_cast<const uint4*>(v_new + src);
     }
-    float kf[8], vf[8];
-    Chunk<T>::to_float(ku, kf);
-    Chunk<T>::to_float(vu, vf);
     uint32_t kw, vw;
-    const uint32_t kn = q4_quantise(kf, lane, &kw);
-    const uint32_t vn = q4_quantise(vf, lane, &vw);
+    const uint32_t kn = q4_quantise<T>(ku, &kw);
+    const uint32_t vn = q4_quantise<T>(vu, &vw);
     if (write) {
       const int64_t tile = ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D);
       const int r = slot & 15;
@@ -170,12 +212,9 @@ __global__ void __launch_bounds__(256)
       ku = *reinterpret_cast<const uint4*>(k_new + src);
       vu = *reinterpret_cast<const uint4*>(v_new + src);
     }
-    float kf[8], vf[8];
-    Chunk<T>::to_float(ku, kf);
-    Chunk<T>::to_float(vu, vf);
     uint32_t kw, vw;
-    const uint32_t kn = q4_quantise(kf, lane, &kw);
-    const uint32_t vn = q4_quantise(vf, lane, &vw);
+    const uint32_t kn = q4_quantise<T>(ku, &kw);
+    const uint32_t vn = q4_quantise<T>(vu, &vw);
     if (write) {
       const int64_t tile = ((int64_t)b * a.heads + h) * q4_tile_bytes(D);
       const int r = (L - 1) % kBlock;
@@ -224,12 +263,9 @@ __global__ void __launch_bounds__(256)
       const int64_t from = ((int64_t)src * heads + h) * wide + row16;
       const uint4 ku = *reinterpret_cast<const uint4*>(k_src + from);
       const uint4 vu = *reinterpret_cast<const uint4*>(v_src + from);
-      float kf[8], vf[8];
-      Chunk<T>::to_float(ku, kf);
-      Chunk<T>::to_float(vu, vf);
       uint32_t kw, vw;
-      const uint32_t kn = q4_quantise(kf, lane, &kw);
-      const uint32_t vn = q4_quantise(vf, lane, &vw);
+      const uint32_t kn = q4_quantise<T>(ku, &kw);
+      const uint32_t vn = q4_quantise<T>(vu, &vw);
       const int64_t tile = ((int64_t)dst * heads + h) * narrow;
       *reinterpret_cast<uint32_t*>(k_dst + tile + q4_data_off(g, j, t)) = kn;
       *reinterpret_cast<uint32_t*>(v_dst + tile + q4_data_off(g, j, t)) = vn;
