@@ -400,8 +400,8 @@ pa_status pa_convert_blocks(const pa_pool* src, const void* k_src, const void* v
  * mass_in, mass_out: fp32 [num_seqs][mass_stride], mass_stride at least the
  * longest context (max_context_len); they may be the same buffer, else they
  * must not overlap; mass_in NULL counts as zero.  Entries at or past a
- * sequence's length are neither read nor written.  The heads are added in
- * order in fp32, so the result does not change from run to run.  All pool
+ * sequence's length are neither read nor written.  The heads are added in a
+ * fixed order in fp32, so the result does not change from run to run.  All pool
  * types.  At most 65535 sequences.
  * workspace: pa_decode_mass_workspace_bytes() (the decode workspace, then 4
  * bytes per query head and token of every sequence's longest context).  The planned form

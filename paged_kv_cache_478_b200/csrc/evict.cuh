@@ -92,17 +92,19 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 }
 
 struct EvictShared {
-  int hist[kEvictBins];
+  alignas(8) int hist[kEvictBins];
   int warp_sums[32];
+  int counts[2][32];  // of each warp's slots
   uint32_t prefix;
   int need;
-  int ties, holes, movers;  // of this CTA's share
+  int done;      // the pass that settled the selection, or -1
+  int total[2];  // of this CTA's share
 };
 
 // One cluster per sequence.  CACHED: the CTA's keys are held in the dynamic
 // shared memory.
 template <bool CACHED>
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_select_kernel(EvictArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t evict_keys[];
   __shared__ EvictShared sh;
@@ -121,14 +123,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
   float* mass_out = a.mass_out + s * a.out_stride;
   int32_t* pos_out = a.positions_out + s * a.out_stride;
   const int held = a.history_in[2 * s], next = a.history_in[2 * s + 1];
-  cluster.sync();  // every CTA of the cluster has read the history before one writes it in place
   // this CTA's slots, each warp's of them contiguous and a multiple of 32
   const int per = (L + C * kEvictThreads - 1) / (C * kEvictThreads) * kEvictThreads;
   const int lo = min(L, rank * per), hi = min(L, lo + per);
   if (keep >= L) {  // nothing to evict
     if (rank == 0 && tid == 0) {
       a.heads[s] = make_int4(0, held, next, 0);
-      a.history_out[2 * s] = held;
+      a.history_out[2 * s] = held;  // as it is: other CTAs may still read it in place
       a.history_out[2 * s + 1] = next;
     }
     if (mass_out != mass)
@@ -149,10 +150,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
   if (tid == 0) {
     sh.prefix = 0;
     sh.need = keep;
+    sh.done = -1;
   }
-  // the keep-th largest key (sh.prefix), and how many tokens of that key stay (sh.need)
-  for (int pass = 0; pass < 3 && keep > 0; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+  // the keep-th largest key, from its first digit on; a pass whose whole bin stays is the last
+  int pass = 0, shift = 0;
+  for (; pass < 3 && keep > 0; ++pass) {
+    shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digit = pass == 2 ? 1023u : 2047u;
     for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
     __syncthreads();
@@ -164,58 +167,77 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
     }
     cluster.sync();
     // two bins a thread, the largest first, summed over the cluster
-    int n[2] = {0, 0};
-    for (int c = 0; c < C; ++c) {
-      const int* h = cluster.map_shared_rank(sh.hist, c);
-      n[0] += h[kEvictBins - 1 - 2 * tid];
-      n[1] += h[kEvictBins - 2 - 2 * tid];
-    }
+    int2 n = make_int2(0, 0);
+#pragma unroll
+    for (int c = 0; c < kEvictMaxCluster; ++c)
+      if (c < C) {
+        const int2 h = reinterpret_cast<const int2*>(cluster.map_shared_rank(sh.hist, c))[kEvictThreads - 1 - tid];
+        n.x += h.y;
+        n.y += h.x;
+      }
     int total;
-    const int above = block_scan(n[0] + n[1], sh.warp_sums, &total);
+    const int above = block_scan(n.x + n.y, sh.warp_sums, &total);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int before = above + (e ? n[0] : 0);
-      if (before < need && need <= before + n[e]) {  // one thread of the block
+      const int before = above + (e ? n.x : 0), in = e ? n.y : n.x;
+      if (before < need && need <= before + in) {  // one thread of the block
         sh.prefix = (prefix << (pass == 2 ? 10 : 11)) | (uint32_t)(kEvictBins - 1 - 2 * tid - e);
         sh.need = need - before;
+        if (need == before + in) sh.done = pass;
       }
     }
     cluster.sync();  // the histograms are free again
+    if (sh.done == pass) break;
   }
-  const uint32_t edge = sh.prefix;
-  const int ties = sh.need;  // of the tokens at the edge, the first this many stay
+  // Keys above `edge` stay, and of those equal to it the first `ties`.  A bin
+  // that stays whole: its lowest key is the edge, without a limit.
+  const uint32_t edge = sh.prefix << shift;
+  const bool whole = sh.done >= 0;
+  const int ties = sh.need;
 
-  // Sums before this CTA over the cluster's shares, of a member of its shared memory.
-  auto before = [&](int EvictShared::* member, int* total) {
-    int sum = 0, all = 0;
-    for (int c = 0; c < C; ++c) {
-      const int v = cluster.map_shared_rank(&sh, c)->*member;
-      sum += c < rank ? v : 0;
-      all += v;
+  const int wlo = lo + warp * (per / 32), whi = min(hi, wlo + per / 32);
+  // Sums of two counts over the warps before this one, in this CTA and in the
+  // cluster's CTAs before it; *all: over the whole cluster.
+  auto sums_before = [&](int2 mine, int2* all) {
+    if (lane == 0) sh.counts[0][warp] = mine.x, sh.counts[1][warp] = mine.y;
+    __syncthreads();
+    const int x = sh.counts[0][lane], y = sh.counts[1][lane];
+    int2 sum = make_int2(__reduce_add_sync(kFullMask, lane < warp ? x : 0), __reduce_add_sync(kFullMask, lane < warp ? y : 0));
+    if (warp == 0) {
+      const int tx = __reduce_add_sync(kFullMask, x), ty = __reduce_add_sync(kFullMask, y);
+      if (lane == 0) sh.total[0] = tx, sh.total[1] = ty;
     }
-    if (total) *total = all;
+    cluster.sync();
+    int2 v = make_int2(0, 0);
+    if (lane < C) {
+      const int* t = cluster.map_shared_rank(sh.total, lane);
+      v = make_int2(t[0], t[1]);
+    }
+    sum.x += __reduce_add_sync(kFullMask, lane < rank ? v.x : 0);
+    sum.y += __reduce_add_sync(kFullMask, lane < rank ? v.y : 0);
+    *all = make_int2(__reduce_add_sync(kFullMask, v.x), __reduce_add_sync(kFullMask, v.y));
     return sum;
   };
-  const int wlo = lo + warp * (per / 32), whi = min(hi, wlo + per / 32);
-  // sweep 1: tokens at the edge
-  int count = 0, total;
-  for (int t0 = wlo; t0 < whi; t0 += 32) {
-    const int t = t0 + lane;
-    count += __popc(__ballot_sync(kFullMask, t < whi && keep > 0 && key(t) == edge));
+  // sweep 1, where not all tokens at the edge stay: their ranks
+  int tie0 = 0;
+  int2 all;
+  if (!whole) {  // the same in every CTA of the cluster
+    int count = 0;
+    for (int t0 = wlo; t0 < whi; t0 += 32) {
+      const int t = t0 + lane;
+      count += __popc(__ballot_sync(kFullMask, t < whi && keep > 0 && key(t) == edge));
+    }
+    tie0 = sums_before(make_int2(count, 0), &all).x;
+    cluster.sync();  // the totals are free again
   }
-  int rank_of_warp = block_scan(lane == 0 ? count : 0, sh.warp_sums, &total);
-  rank_of_warp = __shfl_sync(kFullMask, rank_of_warp, 0);
-  if (tid == 0) sh.ties = total;
-  cluster.sync();
-  const int tie0 = before(&EvictShared::ties, nullptr) + rank_of_warp;
   // Who stays in the 32 slots from t0 on; tie: rank of the first token at the edge.
   auto stays_of = [&](int t0, int& tie) {
     const int t = t0 + lane;
-    const uint32_t k = t < whi && keep > 0 ? key(t) : 0u;
-    const bool at_edge = t < whi && keep > 0 && k == edge;
-    const uint32_t edges = __ballot_sync(kFullMask, at_edge);
-    const bool stays = t < whi && keep > 0 &&
-                       (k > edge || (at_edge && tie + __popc(edges & ((1u << lane) - 1u)) < ties));
+    const bool real = t < whi && keep > 0;
+    const uint32_t k = real ? key(t) : 0u;
+    if (whole) return real && k >= edge;
+    const uint32_t edges = __ballot_sync(kFullMask, real && k == edge);
+    const bool stays = real && (k > edge || (k == edge && tie + __popc(edges & ((1u << lane) - 1u)) < ties));
     tie += __popc(edges);
     return stays;
   };
@@ -227,14 +249,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
     holes += __popc(__ballot_sync(kFullMask, t < whi && t < keep && !stays));
     movers += __popc(__ballot_sync(kFullMask, t >= keep && stays));
   }
-  int hole = block_scan(lane == 0 ? holes : 0, sh.warp_sums, &total);
-  if (tid == 0) sh.holes = total;
-  int mover = block_scan(lane == 0 ? movers : 0, sh.warp_sums, &total);
-  if (tid == 0) sh.movers = total;
-  cluster.sync();
-  int all_movers;
-  hole = before(&EvictShared::holes, nullptr) + __shfl_sync(kFullMask, hole, 0);
-  mover = before(&EvictShared::movers, &all_movers) + __shfl_sync(kFullMask, mover, 0);
+  const int2 first = sums_before(make_int2(holes, movers), &all);
+  int hole = first.x, mover = first.y;
+  const int all_movers = all.y;
   // sweep 3: the moves, and the track of what is not moved
   int2* moves = a.moves + (int64_t)s * a.move_cap;
   tie = tie0;

