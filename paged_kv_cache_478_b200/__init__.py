@@ -156,10 +156,19 @@ def _check(status: int):
 
 # ---- torch marshalling -------------------------------------------------------------
 
-def _torch():
-    import torch
+_torch_module = None
+_TORCH_DTYPES = {}  # PA_* code -> torch dtype of q, out, k_new and v_new
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _TORCH_DTYPES.update({PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16,
+                              PA_Q4_F16: torch.float16, PA_Q4_BF16: torch.bfloat16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
@@ -175,14 +184,19 @@ def _dev_ptr(t, name, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    if t.get_device() != torch.cuda.current_device():  # the launch goes to the current device
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.data_ptr()
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object in between
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def pa_pool_create(num_blocks: int, block_size: int, heads: int, head_dim: int, dtype) -> pa_pool:
@@ -205,9 +219,8 @@ def _q_heads(pool: pa_pool) -> int:
 
 
 def _pool_torch_dtype(pool: pa_pool):
-    torch = _torch()
-    return {PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16,
-            PA_Q4_F16: torch.float16, PA_Q4_BF16: torch.bfloat16}[pool.dtype]
+    _torch()
+    return _TORCH_DTYPES[pool.dtype]
 
 
 def _check_pool_tensor(pool, t, name):
