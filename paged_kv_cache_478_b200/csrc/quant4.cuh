@@ -74,59 +74,76 @@ __device__ __forceinline__ float q4_quotient(float x, float inv) {
   return __fadd_rn(h, kRoundMagic);
 }
 
-// Quantise one group of 64 values held by 8 neighbouring lanes, 8 each (all
-// 32 lanes of the warp call).  Returns the lane's 8 numbers, the first in the
-// lowest 4 bits; *word is the group's word.  The largest and smallest value are
-// found in the 16-bit type, NaN winning, as one pair (max, -min) across the
-// lanes.
+// The largest value of a group and the smallest, negated, as a pair in the
+// 16-bit type, NaN winning: the same in all of the group's 8 lanes.
 template <typename T>
-__device__ __forceinline__ uint32_t q4_quantise(const uint4& u, uint32_t* word) {
+__device__ __forceinline__ uint32_t q4_extent(const uint4& u) {
   using P = Pair<T>;
   using V = typename P::V;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   auto as_v = [](uint32_t x) { return *reinterpret_cast<const V*>(&x); };
   auto as_u = [](V x) { return *reinterpret_cast<uint32_t*>(&x); };
-  const V m = P::max_nan(P::max_nan(as_v(w[0]), as_v(w[1])), P::max_nan(as_v(w[2]), as_v(w[3])));
-  const V l = P::min_nan(P::min_nan(as_v(w[0]), as_v(w[1])), P::min_nan(as_v(w[2]), as_v(w[3])));
+  const V m = P::max_nan(P::max_nan(as_v(u.x), as_v(u.y)), P::max_nan(as_v(u.z), as_v(u.w)));
+  const V l = P::min_nan(P::min_nan(as_v(u.x), as_v(u.y)), P::min_nan(as_v(u.z), as_v(u.w)));
   const uint32_t mu = as_u(m), lu = as_u(l) ^ 0x80008000u;
   V top = P::max_nan(as_v(__byte_perm(mu, lu, 0x5410)), as_v(__byte_perm(mu, lu, 0x7632)));
 #pragma unroll
   for (int k = 1; k < 8; k <<= 1) top = P::max_nan(top, as_v(__shfl_xor_sync(kFullMask, as_u(top), k)));
-  const float2 ends = P::floats(top);
-  const float hi = ends.x, lo = -ends.y;
-  float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
-  const float big = fmaxf(fabsf(hi), fabsf(lo));
-  if (big > 1990.f * raw) raw = fmaxf(raw, __fdiv_rn(big, 2000.f));  // the other quotient may be the larger
-  const float s = __bfloat162float(__float2bfloat16_rn(raw));
-  if (!(s < INFINITY)) {
-    *word = 0x7fc00000u;  // s = NaN, z = 0
-    return 0u;
-  }
-  if (s == 0.f) {
-    *word = 0u;
-    return 0u;
-  }
+  return as_u(top);
+}
+
+// A lane's 8 numbers, the first in the lowest 4 bits, given the group's
+// scale, its reciprocal and zero point.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_numbers(const uint4& u, float s, float inv, float z) {
+  if (!(s > 0.f)) return 0u;  // a group of zeros, or s = NaN
   float x[8];
   Chunk<T>::to_float(u, x);
   uint32_t n = 0;
   if (s < 1e-36f) {  // 1 / s or a product may leave the normal numbers: divide
-    const float z = rintf(__fdiv_rn(-lo, s)) + 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + z, 0.f), 15.f);
       n |= (uint32_t)v << (4 * e);
     }
-    *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
     return n;
   }
-  const float inv = __frcp_rn(s);
-  const float z = __fsub_rn(q4_quotient(-lo, inv), kRoundMagic);
   const int off = (int)z - __float_as_int(kRoundMagic);
 #pragma unroll
   for (int e = 0; e < 8; ++e)  // clamp(round(x / s) + z, 0, 15)
     n += (uint32_t)__viaddmin_s32_relu(__float_as_int(q4_quotient(x[e], inv)), off, 15) << (4 * e);
-  *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
   return n;
+}
+
+// Quantise a K and a V group of 64 values, each held by 8 neighbouring lanes,
+// 8 each (all 32 lanes of the warp call).  *kn and *vn are the lane's numbers;
+// *word is the K group's word in lanes 0 .. 3 of the 8 and the V group's in
+// lanes 4 .. 7, which work out one of the two scales each.
+template <typename T>
+__device__ __forceinline__ void q4_quantise(const uint4& k, const uint4& v, int lane, uint32_t* kn,
+                                            uint32_t* vn, uint32_t* word) {
+  using V = typename Pair<T>::V;
+  const uint32_t ke = q4_extent<T>(k), ve = q4_extent<T>(v);
+  const uint32_t mine = (lane & 4) ? ve : ke;
+  const float2 ends = Pair<T>::floats(*reinterpret_cast<const V*>(&mine));
+  const float hi = ends.x, lo = -ends.y;
+  float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
+  const float big = fmaxf(fabsf(hi), fabsf(lo));
+  if (big > 1990.f * raw) raw = fmaxf(raw, __fdiv_rn(big, 2000.f));  // the other quotient may be the larger
+  float s = __bfloat162float(__float2bfloat16_rn(raw));
+  if (!(s < INFINITY)) s = __uint_as_float(0x7fc00000u);
+  float inv = 0.f, z = 0.f;
+  if (s >= 1e-36f) {
+    inv = __frcp_rn(s);
+    z = __fsub_rn(q4_quotient(-lo, inv), kRoundMagic);
+  } else if (s > 0.f) {
+    z = rintf(__fdiv_rn(-lo, s)) + 0.f;
+  }
+  *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
+  const float s2 = __shfl_xor_sync(kFullMask, s, 4), inv2 = __shfl_xor_sync(kFullMask, inv, 4);
+  const float z2 = __shfl_xor_sync(kFullMask, z, 4);
+  const bool own_v = (lane & 4) != 0;
+  *kn = q4_numbers<T>(k, own_v ? s2 : s, own_v ? inv2 : inv, own_v ? z2 : z);
+  *vn = q4_numbers<T>(v, own_v ? s : s2, own_v ? inv : inv2, own_v ? z : z2);
 }
 
 // Where the lane's 8 numbers of (row t, group g) go in a tile: lane j of the
@@ -165,18 +182,15 @@ __global__ void __launch_bounds__(256)
       ku = *reinterpret_cast<const uint4*>(k_new + src);
       vu = *reinterpret_cast<const uint4*>(v_new + src);
     }
-    uint32_t kw, vw;
-    const uint32_t kn = q4_quantise<T>(ku, &kw);
-    const uint32_t vn = q4_quantise<T>(vu, &vw);
+    uint32_t kn, vn, word;
+    q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
     if (write) {
       const int64_t tile = ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D);
       const int r = slot & 15;
       *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g, j, r)) = kn;
       *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g, j, r)) = vn;
-      if (j == 0) {
-        *reinterpret_cast<uint32_t*>(k_pool + tile + q4_words_off(D) + (g * 16 + r) * 4) = kw;
-        *reinterpret_cast<uint32_t*>(v_pool + tile + q4_words_off(D) + (g * 16 + r) * 4) = vw;
-      }
+      if ((j & 3) == 0)
+        *reinterpret_cast<uint32_t*>((j == 0 ? k_pool : v_pool) + tile + q4_words_off(D) + (g * 16 + r) * 4) = word;
     }
   }
 }
@@ -212,9 +226,8 @@ __global__ void __launch_bounds__(256)
       ku = *reinterpret_cast<const uint4*>(k_new + src);
       vu = *reinterpret_cast<const uint4*>(v_new + src);
     }
-    uint32_t kw, vw;
-    const uint32_t kn = q4_quantise<T>(ku, &kw);
-    const uint32_t vn = q4_quantise<T>(vu, &vw);
+    uint32_t kn, vn, word;
+    q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
     if (write) {
       const int64_t tile = ((int64_t)b * a.heads + h) * q4_tile_bytes(D);
       const int r = (L - 1) % kBlock;
@@ -222,10 +235,8 @@ __global__ void __launch_bounds__(256)
       uint8_t* vt = static_cast<uint8_t*>(const_cast<void*>(a.v_pool)) + tile;
       *reinterpret_cast<uint32_t*>(kt + q4_data_off(g, j, r)) = kn;
       *reinterpret_cast<uint32_t*>(vt + q4_data_off(g, j, r)) = vn;
-      if (j == 0) {
-        *reinterpret_cast<uint32_t*>(kt + q4_words_off(D) + (g * 16 + r) * 4) = kw;
-        *reinterpret_cast<uint32_t*>(vt + q4_words_off(D) + (g * 16 + r) * 4) = vw;
-      }
+      if ((j & 3) == 0)
+        *reinterpret_cast<uint32_t*>((j == 0 ? kt : vt) + q4_words_off(D) + (g * 16 + r) * 4) = word;
     }
   }
 }
@@ -263,16 +274,13 @@ __global__ void __launch_bounds__(256)
       const int64_t from = ((int64_t)src * heads + h) * wide + row16;
       const uint4 ku = *reinterpret_cast<const uint4*>(k_src + from);
       const uint4 vu = *reinterpret_cast<const uint4*>(v_src + from);
-      uint32_t kw, vw;
-      const uint32_t kn = q4_quantise<T>(ku, &kw);
-      const uint32_t vn = q4_quantise<T>(vu, &vw);
+      uint32_t kn, vn, word;
+      q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
       const int64_t tile = ((int64_t)dst * heads + h) * narrow;
       *reinterpret_cast<uint32_t*>(k_dst + tile + q4_data_off(g, j, t)) = kn;
       *reinterpret_cast<uint32_t*>(v_dst + tile + q4_data_off(g, j, t)) = vn;
-      if (j == 0) {
-        *reinterpret_cast<uint32_t*>(k_dst + tile + q4_words_off(D) + (g * 16 + t) * 4) = kw;
-        *reinterpret_cast<uint32_t*>(v_dst + tile + q4_words_off(D) + (g * 16 + t) * 4) = vw;
-      }
+      if ((j & 3) == 0)
+        *reinterpret_cast<uint32_t*>((j == 0 ? k_dst : v_dst) + tile + q4_words_off(D) + (g * 16 + t) * 4) = word;
     } else {
       const int64_t tile = ((int64_t)src * heads + h) * narrow;
       const int64_t to = ((int64_t)dst * heads + h) * wide + row16;
