@@ -558,11 +558,11 @@ cudaError_t launch_grouped(int G, const DecodeArgs& a, const DeviceState& dev, c
   }
 }
 
-// Quantise new tokens into a 4-bit pool: eight lanes per (token, head, 64 dimensions).
+// Quantise new tokens into a 4-bit pool: eight lanes per (token, head, 64 dimensions), two of those each.
 pa_status launch_q4_append(const DeviceState& dev, const pa_pool* pool, const void* k_new,
                            const void* v_new, const int32_t* slots, int32_t num_tokens, void* k_pool,
                            void* v_pool, cudaStream_t s) {
-  const int64_t threads = (int64_t)num_tokens * pool->heads * (pool->head_dim / 64) * 8;
+  const int64_t threads = (int64_t)num_tokens * pool->heads * (pool->head_dim / 64) * 4;
   const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev.num_sms * 8);
   auto kp = static_cast<uint8_t*>(k_pool), vp = static_cast<uint8_t*>(v_pool);
   const int64_t num_slots = pool->num_blocks * pool->block_size;
@@ -1268,7 +1268,7 @@ pa_status pa_convert_blocks(const pa_pool* src, const void* k_src, const void* v
     return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: pools must be 16-byte aligned");
   DeviceState* dev;
   if ((st = device_state(&dev)) != PA_OK) return st;
-  const int64_t threads = (int64_t)num_pairs * src->heads * (src->head_dim / 64) * kBlock * 8;
+  const int64_t threads = (int64_t)num_pairs * src->heads * 32;  // a warp per (pair, head)
   const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev->num_sms * 8);
   auto kernel = src->dtype == PA_F16       ? q4_convert_kernel<__half, true>
                 : src->dtype == PA_BF16    ? q4_convert_kernel<__nv_bfloat16, true>

@@ -152,45 +152,58 @@ __device__ __forceinline__ int q4_data_off(int g, int j, int t) {
   return (2 * g + (j >> 2)) * 256 + t * 16 + (j & 3) * 4;
 }
 
+// a / b, by 32-bit division where both fit (a 64-bit one costs as much as
+// quantising four values).
+__device__ __forceinline__ int64_t q4_div(int64_t a, int b) {
+  return a <= 0xffffffffll ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Append: each new token's K and V rows are quantised into the slot that
-// slot_mapping names.  Eight lanes take one (token, head, group of 64): one
-// 16-byte load of K and of V per lane, one 4-byte store each.
+// slot_mapping names.  Eight lanes take one (token, head, group of 64), a warp
+// U x 4 neighbouring ones a round, their loads in flight together: one 16-byte
+// load of K and of V per lane, one 4-byte store each.
 template <typename T>
 __global__ void __launch_bounds__(256)
     q4_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new,
                      const int32_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_pool,
                      uint8_t* __restrict__ v_pool, int heads, int D, int64_t num_tokens,
                      int64_t num_slots, uint32_t* err) {
+  constexpr int U = 2;
   const int lane = threadIdx.x & 31, j = lane & 7;
   const int groups = D / 64;
   const int64_t total = num_tokens * heads * groups;
   // every lane of a warp runs the same number of rounds (the shuffles need all of them)
-  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
+  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 * U < total;
        w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t u = w * 4 + (lane >> 3);
-    const bool live = u < total;
-    const int64_t row = live ? u / groups : 0;  // token * heads + head
-    const int g = live ? (int)(u - row * groups) : 0;
-    const int64_t t = row / heads;
-    const int h = (int)(row - t * heads);
-    const int32_t slot = live ? slot_mapping[t] : -1;
-    if (slot >= num_slots && h == 0 && g == 0 && j == 0) atomicOr(err, PA_DEVERR_SLOT);
-    const bool write = slot >= 0 && slot < num_slots;  // a negative slot is padding
-    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-    if (write) {
-      const int64_t src = row * D + g * 64 + j * 8;
-      ku = *reinterpret_cast<const uint4*>(k_new + src);
-      vu = *reinterpret_cast<const uint4*>(v_new + src);
+    uint4 ku[U], vu[U];
+    int32_t slot[U];
+    int h[U], g[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t u = (w * U + i) * 4 + (lane >> 3);
+      const bool live = u < total;
+      const int64_t row = live ? u >> (groups - 1) : 0;  // token * heads + head; groups is 1 or 2
+      g[i] = live ? (int)(u - row * groups) : 0;
+      const int64_t t = q4_div(row, heads);
+      h[i] = (int)(row - t * heads);
+      slot[i] = live ? slot_mapping[t] : -1;
+      const int64_t src = row * D + g[i] * 64 + j * 8;
+      ku[i] = *reinterpret_cast<const uint4*>(k_new + src);
+      vu[i] = *reinterpret_cast<const uint4*>(v_new + src);
     }
-    uint32_t kn, vn, word;
-    q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
-    if (write) {
-      const int64_t tile = ((int64_t)(slot >> 4) * heads + h) * q4_tile_bytes(D);
-      const int r = slot & 15;
-      *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g, j, r)) = kn;
-      *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g, j, r)) = vn;
-      if ((j & 3) == 0)
-        *reinterpret_cast<uint32_t*>((j == 0 ? k_pool : v_pool) + tile + q4_words_off(D) + (g * 16 + r) * 4) = word;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (slot[i] >= num_slots && h[i] == 0 && g[i] == 0 && j == 0) atomicOr(err, PA_DEVERR_SLOT);
+      uint32_t kn, vn, word;
+      q4_quantise<T>(ku[i], vu[i], lane, &kn, &vn, &word);
+      if (slot[i] >= 0 && slot[i] < num_slots) {  // a negative slot is padding
+        const int64_t tile = ((int64_t)(slot[i] >> 4) * heads + h[i]) * q4_tile_bytes(D);
+        const int r = slot[i] & 15;
+        *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g[i], j, r)) = kn;
+        *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g[i], j, r)) = vn;
+        if ((j & 3) == 0)
+          *reinterpret_cast<uint32_t*>((j == 0 ? k_pool : v_pool) + tile + q4_words_off(D) + (g[i] * 16 + r) * 4) = word;
+      }
     }
   }
 }
@@ -209,9 +222,9 @@ __global__ void __launch_bounds__(256)
        w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
     const int64_t u = w * 4 + (lane >> 3);
     const bool live = u < total;
-    const int64_t row = live ? u / groups : 0;  // sequence * heads + head
+    const int64_t row = live ? u >> (groups - 1) : 0;  // sequence * heads + head
     const int g = live ? (int)(u - row * groups) : 0;
-    const int s = (int)(row / a.heads);
+    const int s = (int)q4_div(row, a.heads);
     const int h = (int)(row - (int64_t)s * a.heads);
     const int L = live ? a.lens[s] : 0;
     bool write = L > 0 && L <= cap;
@@ -242,66 +255,87 @@ __global__ void __launch_bounds__(256)
 }
 
 // Whole blocks from a 16-bit pool into a 4-bit one (PACK) or back, for every
-// (src, dst) pair.  Eight lanes take one (pair, head, group, token); tokens
-// are innermost, so the stores of a warp's four tokens are contiguous.
+// (src, dst) pair.  A warp takes a (pair, head) tile, 4 tokens of one group of 64
+// dimensions a step, 8 lanes a token: 16-byte loads or stores of the wide rows,
+// 4-byte ones of the pieces, of which a step's four tokens are contiguous.  The
+// loads of U steps are in flight together.
 template <typename T, bool PACK>
 __global__ void __launch_bounds__(256)
     q4_convert_kernel(const uint8_t* __restrict__ k_src, const uint8_t* __restrict__ v_src,
                       uint8_t* __restrict__ k_dst, uint8_t* __restrict__ v_dst,
                       const int32_t* __restrict__ pairs, int64_t num_pairs, int64_t src_blocks,
                       int64_t dst_blocks, int heads, int D, uint32_t* err) {
+  constexpr int U = PACK ? 2 : 4;
   const int lane = threadIdx.x & 31, j = lane & 7;
-  const int groups = D / 64;
-  const int64_t total = num_pairs * heads * groups * kBlock;  // a multiple of 4
+  const int groups = D / 64, steps = 4 * groups;
   const int64_t wide = (int64_t)kBlock * D * sizeof(T);
   const int narrow = q4_tile_bytes(D);
-  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
-       w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t u = w * 4 + (lane >> 3);
-    const int t = (int)(u % kBlock);
-    int64_t rest = u / kBlock;
-    const int g = (int)(rest % groups);
-    rest /= groups;
-    const int h = (int)(rest % heads);
-    const int64_t p = rest / heads;
+  const int64_t tiles = num_pairs * heads, warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t tile = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; tile < tiles; tile += warps) {
+    const int64_t p = q4_div(tile, heads);
+    const int h = (int)(tile - p * heads);
     const int32_t src = pairs[2 * p], dst = pairs[2 * p + 1];
-    if (src < 0 || src >= src_blocks || dst < 0 || dst >= dst_blocks) {  // the same for the warp
-      if (h == 0 && g == 0 && t == 0 && j == 0) atomicOr(err, PA_DEVERR_PAIR);
+    if (src < 0 || src >= src_blocks || dst < 0 || dst >= dst_blocks) {
+      if (h == 0 && lane == 0) atomicOr(err, PA_DEVERR_PAIR);
       continue;
     }
-    const int64_t row16 = (int64_t)t * D * sizeof(T) + (g * 64 + j * 8) * sizeof(T);
-    if constexpr (PACK) {
-      const int64_t from = ((int64_t)src * heads + h) * wide + row16;
-      const uint4 ku = *reinterpret_cast<const uint4*>(k_src + from);
-      const uint4 vu = *reinterpret_cast<const uint4*>(v_src + from);
-      uint32_t kn, vn, word;
-      q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
-      const int64_t tile = ((int64_t)dst * heads + h) * narrow;
-      *reinterpret_cast<uint32_t*>(k_dst + tile + q4_data_off(g, j, t)) = kn;
-      *reinterpret_cast<uint32_t*>(v_dst + tile + q4_data_off(g, j, t)) = vn;
-      if ((j & 3) == 0)
-        *reinterpret_cast<uint32_t*>((j == 0 ? k_dst : v_dst) + tile + q4_words_off(D) + (g * 16 + t) * 4) = word;
-    } else {
-      const int64_t tile = ((int64_t)src * heads + h) * narrow;
-      const int64_t to = ((int64_t)dst * heads + h) * wide + row16;
-      // the largest finite value of T: the last step of a group may pass it
-      constexpr float kTop = std::is_same<T, __half>::value ? 65504.f : 3.38953139e38f;
-      auto one = [&](const uint8_t* from, uint8_t* into) {
-        const uint32_t n = *reinterpret_cast<const uint32_t*>(from + tile + q4_data_off(g, j, t));
-        const uint32_t word =
-            *reinterpret_cast<const uint32_t*>(from + tile + q4_words_off(D) + (g * 16 + t) * 4);
-        const float s = q4_scale(word), z = q4_zero(word);
-        float f[8];
+    const int64_t from = ((int64_t)src * heads + h) * (PACK ? wide : narrow);
+    const int64_t to = ((int64_t)dst * heads + h) * (PACK ? narrow : wide);
+    const uint8_t *k_in = k_src + from, *v_in = v_src + from;
+    uint8_t *k_out = k_dst + to, *v_out = v_dst + to;
+    for (int i0 = 0; i0 < steps; i0 += U) {
+      int g[U], t[U], row16[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // exact in fp32 (8 by 12 bits), rounded once to T below
-          const float v = s * ((float)((n >> (4 * e)) & 15u) - z);
-          f[e] = v > kTop ? kTop : v < -kTop ? -kTop : v;  // NaN stays
+      for (int u = 0; u < U; ++u) {
+        g[u] = (i0 + u) >> 2;
+        t[u] = ((i0 + u) & 3) * 4 + (lane >> 3);
+        row16[u] = (t[u] * D + g[u] * 64 + j * 8) * (int)sizeof(T);
+      }
+      if constexpr (PACK) {
+        uint4 ku[U], vu[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          ku[u] = *reinterpret_cast<const uint4*>(k_in + row16[u]);
+          vu[u] = *reinterpret_cast<const uint4*>(v_in + row16[u]);
         }
-        *reinterpret_cast<uint4*>(into + to) = Chunk<T>::from_float(f);
-      };
-      one(k_src, k_dst);
-      one(v_src, v_dst);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          uint32_t kn, vn, word;
+          q4_quantise<T>(ku[u], vu[u], lane, &kn, &vn, &word);
+          *reinterpret_cast<uint32_t*>(k_out + q4_data_off(g[u], j, t[u])) = kn;
+          *reinterpret_cast<uint32_t*>(v_out + q4_data_off(g[u], j, t[u])) = vn;
+          if ((j & 3) == 0)
+            *reinterpret_cast<uint32_t*>((j == 0 ? k_out : v_out) + q4_words_off(D) + (g[u] * 16 + t[u]) * 4) = word;
+        }
+      } else {
+        // the largest finite value of T: the last step of a group may pass it
+        constexpr float kTop = std::is_same<T, __half>::value ? 65504.f : 3.38953139e38f;
+        uint32_t n[U][2], word[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int data = q4_data_off(g[u], j, t[u]), w = q4_words_off(D) + (g[u] * 16 + t[u]) * 4;
+          n[u][0] = *reinterpret_cast<const uint32_t*>(k_in + data);
+          n[u][1] = *reinterpret_cast<const uint32_t*>(v_in + data);
+          word[u][0] = *reinterpret_cast<const uint32_t*>(k_in + w);
+          word[u][1] = *reinterpret_cast<const uint32_t*>(v_in + w);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const float s = q4_scale(word[u][kv]), z = q4_zero(word[u][kv]);
+            const float base = 8388608.f + z;  // 2^23 + z: exact for the whole numbers that z may be
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)  // exact in fp32 (8 by 12 bits), rounded once to T below
+              f[e] = s * (__uint_as_float(0x4b000000u | ((n[u][kv] >> (4 * e)) & 15u)) - base);
+            if (!(fabsf(s) * fmaxf(15.f + z, 15.f - z) <= kTop)) {  // a value may pass the range, or s is NaN
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = f[e] > kTop ? kTop : f[e] < -kTop ? -kTop : f[e];  // NaN stays
+            }
+            *reinterpret_cast<uint4*>((kv ? v_out : k_out) + row16[u]) = Chunk<T>::from_float(f);
+          }
+      }
     }
   }
 }
