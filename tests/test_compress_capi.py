@@ -108,3 +108,21 @@ def test_evict_refusals():
     need = pa.pa_evict_workspace_bytes(p, 1, 4)
     assert call(size=need - 1) == 6
     assert call(S=0) == 0
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The launch goes to the current device: a tensor elsewhere is refused before any call."""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    t = torch.zeros(4).as_subclass(Elsewhere)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        pa._dev_ptr(t, "t")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert pa._dev_ptr(t, "t") == t.data_ptr()

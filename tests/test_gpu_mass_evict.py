@@ -363,3 +363,64 @@ def test_decode_gather_evict_loop(kind):
                     kept = set(pos[s, :budget].tolist())
                     assert {0, 1} <= kept and set(range(total[s] - 8, total[s])) <= kept
     assert evictions >= 3
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "q4_f16"])
+def test_mass_in_a_graph(kind):
+    """Plan, attention and gathering captured together and replayed: every replay decays and adds once more."""
+    c = any_case(21, [40, 0, 333], 2, 2 if kind != "f32" else 1, 64, kind)
+    pool = pool_of(c)
+    bt, cl = cuda(c["tables"]), cuda(c["lens"])
+    ws = mass_workspace(pool, 3, bt.shape[1])
+    out, mass = torch.empty_like(c["q"]), torch.zeros((3, bt.shape[1] * 16), device="cuda")
+    step = lambda m: pa.pa_decode_attention_mass(pool, c["q"], c["k"], c["v"], bt, cl, c["scale"], out, m, m, ws, decay=0.5)  # noqa: E731
+    want = torch.zeros_like(mass)
+    for _ in range(3):
+        step(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step(mass)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(mass, want) and pa.pa_device_errors() == 0
+
+
+def test_evict_of_a_very_long_sequence():
+    """More keys than the cluster's shared memory holds: the track is read anew each pass."""
+    rng = np.random.default_rng(22)
+    L, keep = 400001, 123457
+    c = any_case_bytes(rng, [L], 1, 64, "q4_bf16")
+    state = evict_state(rng, [L], [keep], c["tables"].shape[1] * 16, ties=True)
+    for inplace in (False, True):
+        k, v = c["k"].clone(), c["v"].clone()
+        after = run_evict(c, [keep], 4, 5000, state, inplace, k, v)
+        moves, mass, positions, history = oc.evict(state[0][0], state[1][0], state[2][0], L, keep, 4, 5000)
+        assert np.array_equal(after["mass"][0, :L].cpu().numpy(), np.array(mass[:L], dtype=np.float32), equal_nan=True)
+        assert np.array_equal(after["positions"][0, :keep].cpu().numpy(), positions[:keep])
+        assert tuple(after["history"][0].cpu().numpy()) == history
+        want = rows_of(c["k"], 64)
+        src, dst = np.array([m[0] for m in moves]), np.array([m[1] for m in moves])
+        want[c["tables"][0, dst // 16], :, dst % 16] = want[c["tables"][0, src // 16], :, src % 16]
+        assert np.array_equal(rows_of(k, 64), want)
+
+
+def test_evict_offsets_past_32_bits():
+    """Rows moved in the last blocks of a pool of more than 2^32 bytes."""
+    rng = np.random.default_rng(23)
+    heads, dim, nb = 32, 128, 34000
+    c = any_case_bytes(rng, [90], heads, dim, "f16")
+    small = c["k"].shape[0]
+    state = evict_state(rng, [90], [30], 96)
+    k, v = c["k"].clone(), c["v"].clone()
+    run_evict(c, [30], 1, 5, state, False, k, v)
+    big_k = torch.zeros((nb, heads, 16, dim), dtype=torch.float16, device="cuda")
+    assert big_k.numel() * 2 > 2 ** 32
+    big_v = torch.zeros_like(big_k)
+    big_k[-small:], big_v[-small:] = c["k"], c["v"]
+    far = dict(c, k=big_k, tables=np.where(c["tables"] >= 0, c["tables"] + nb - small, -1).astype(np.int32))
+    run_evict(far, [30], 1, 5, state, False, big_k, big_v)
+    assert torch.equal(big_k[-small:].view(torch.uint8), k.view(torch.uint8))
+    assert torch.equal(big_v[-small:].view(torch.uint8), v.view(torch.uint8)) and not big_k[:-small].any()

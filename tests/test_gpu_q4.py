@@ -417,3 +417,71 @@ def test_wrong_tensors_are_refused_by_the_binding():
         pa.pa_reshape_and_cache(pool, new, new, slot, k.view(torch.int8), k)
     with pytest.raises(TypeError):
         pa.pa_reshape_and_cache(pool, new.bfloat16(), new, slot, k, k)
+
+
+def test_two_streams_at_once():
+    """Two decode calls in flight together, each with its own workspace and output."""
+    cases = [decode_case(15, [300, 40], 4, 2, 128, "f16"), decode_case(16, [90, 500, 1], 2, 8, 64, "bf16")]
+    want = [run_decode(c, 64) for c in cases]
+    streams, got, keep = [torch.cuda.Stream() for _ in cases], [], []
+    for c, st in zip(cases, streams):
+        pool = pa.pa_pool_set_query_heads(pa.pa_pool_create(c["kp"].shape[0], 16, c["heads"], c["dim"], TYPES[c["kind"]][1]), c["heads"] * c["group"])
+        args = [cuda(c[k]) for k in ("kp", "vp", "tables", "lens")]
+        keep.append((pool, args, workspace_for(pool, len(c["lens"]), c["tables"].shape[1], 0, 64), torch.empty_like(c["q"])))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, st, (pool, (k, v, bt, cl), ws, out) in zip(cases, streams, keep):
+            pa.pa_decode_attention(pool, c["q"], k, v, bt, cl, c["scale"], out, ws, partition_size=64, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, _, out), w in zip(keep, want):
+        assert torch.equal(out, w)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes: append, attention, copy and conversion in its last blocks
+    give what they give in a small pool."""
+    heads, dim, nb = 32, 128, 120000
+    assert nb * heads * 9 * dim > 2 ** 32
+    c = decode_case(17, [70, 33], heads, 1, dim, "f16")
+    want = run_decode(c)
+    small = c["kp"].shape[0]
+    k = torch.zeros((nb, heads, 9 * dim), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    k[-small:], v[-small:] = cuda(c["kp"]), cuda(c["vp"])
+    far = dict(c, tables=np.where(c["tables"] >= 0, c["tables"] + nb - small, -1).astype(np.int32))
+    pool = pa.pa_pool_create(nb, 16, heads, dim, pa.PA_Q4_F16)
+    out = torch.empty_like(c["q"])
+    ws = workspace_for(pool, 2, c["tables"].shape[1])
+    pa.pa_decode_attention(pool, c["q"], k, v, cuda(far["tables"]), cuda(c["lens"]), c["scale"], out, ws)
+    assert torch.equal(out, want)
+    wide = pa.pa_pool_create(2, 16, heads, dim, torch.float16)
+    x = torch.randn((2, heads, 16, dim), dtype=torch.float16, device="cuda")
+    back = torch.zeros_like(x)
+    pa.pa_convert_blocks(wide, x, x, pool, k, v, torch.tensor([[0, nb - 1], [1, 3]], dtype=torch.int32, device="cuda"))
+    pa.pa_convert_blocks(pool, k, v, wide, back, torch.zeros_like(x), torch.tensor([[nb - 1, 1], [3, 0]], dtype=torch.int32, device="cuda"))
+    assert (back.flip(0) - x).abs().max() <= 0.5  # a step of N(0, 1) rows is about 0.3
+    pa.pa_copy_blocks(pool, k, v, torch.tensor([[nb - 1, nb - 2]], dtype=torch.int32, device="cuda"))
+    assert torch.equal(k[nb - 2], k[nb - 1]) and k[nb - 1].any()
+    new = x[0, :, :1].permute(1, 0, 2).contiguous()
+    pa.pa_reshape_and_cache(pool, new, new, torch.tensor([(nb - 2) * 16 + 5], dtype=torch.int32, device="cuda"), k, v)
+    row = oc.values(k[nb - 2:nb - 1].cpu().numpy(), dim)[0, :, 5]
+    assert np.abs(row - new[0].double().cpu().numpy()).max() <= 0.5
+    assert pa.pa_device_errors() == 0
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_append_far_from_zero(kind):
+    """Groups whose offset is many times their range: quotients up to 2000, halves among them."""
+    rng = np.random.default_rng(18)
+    T, dim = 512, 64
+    x = rng.integers(-2000, 2000, (T, 1, 1)) * 0.5 + rng.integers(0, 64, (T, 1, dim)) * 0.25
+    kn, kx = as_type(x, kind)
+    vn, vx = as_type(x[::-1] * 2.0 ** rng.integers(-10, 3, (T, 1, 1)), kind)
+    pool = pa.pa_pool_create(T // 16, 16, 1, dim, TYPES[kind][1])
+    kd, vd = torch.zeros((T // 16, 1, 9 * dim), dtype=torch.uint8, device="cuda"), torch.zeros((T // 16, 1, 9 * dim), dtype=torch.uint8, device="cuda")
+    pa.pa_reshape_and_cache(pool, kn, vn, torch.arange(T, dtype=torch.int32, device="cuda"), kd, vd)
+    kp, vp = np.zeros(kd.shape, dtype=np.uint8), np.zeros(kd.shape, dtype=np.uint8)
+    for t in range(T):
+        oc.store_row(kp, t // 16, 0, t % 16, kx[t, 0])
+        oc.store_row(vp, t // 16, 0, t % 16, vx[t, 0])
+    assert np.array_equal(kd.cpu().numpy(), kp) and np.array_equal(vd.cpu().numpy(), vp)
