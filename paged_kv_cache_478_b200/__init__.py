@@ -157,14 +157,17 @@ def _check(status: int):
 # ---- torch marshalling -------------------------------------------------------------
 
 _torch_module = None
+_current_device = None  # index of the current CUDA device, set with the module
 _TORCH_DTYPES = {}  # PA_* code -> torch dtype of q, out, k_new and v_new
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _current_device
     if _torch_module is None:
         import torch
 
+        # the call behind torch.cuda.current_device(), which tensors have initialised by then
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _TORCH_DTYPES.update({PA_F32: torch.float32, PA_F16: torch.float16, PA_BF16: torch.bfloat16,
                               PA_Q4_F16: torch.float16, PA_Q4_BF16: torch.bfloat16})
         _torch_module = torch
@@ -184,7 +187,7 @@ def _dev_ptr(t, name, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != torch.cuda.current_device():  # the launch goes to the current device
+    if t.get_device() != _current_device():  # the launch goes to the current device
         raise ValueError(f"{name} must be on the current CUDA device")
     return t.data_ptr()
 
@@ -195,7 +198,7 @@ def _stream(stream):
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object in between
     if raw is not None:
-        return raw(torch.cuda.current_device())
+        return raw(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -227,7 +230,7 @@ def _check_pool_tensor(pool, t, name):
     q4 = pool.dtype in (PA_Q4_F16, PA_Q4_BF16)
     shape = ((pool.num_blocks, pool.heads, 9 * pool.head_dim) if q4 else
              (pool.num_blocks, pool.heads, pool.block_size, pool.head_dim))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return _dev_ptr(t, name, _torch().uint8 if q4 else _pool_torch_dtype(pool))
 
@@ -269,7 +272,7 @@ def pa_decode_attention(pool, q, k_pool, v_pool, block_tables, context_lens, sca
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
         _dev_ptr(context_lens, "context_lens", torch.int32), S, max_context_len, float(scale),
         _dev_ptr(out, "out", dt), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), partition_size, _stream(stream)))
+        workspace.nbytes, partition_size, _stream(stream)))
 
 
 def pa_decode_plan(pool, context_lens, max_blocks_per_seq, workspace, max_context_len=0,
@@ -278,7 +281,7 @@ def pa_decode_plan(pool, context_lens, max_blocks_per_seq, workspace, max_contex
     _check(lib().pa_decode_plan(
         ctypes.byref(pool), _dev_ptr(context_lens, "context_lens", torch.int32),
         context_lens.shape[0], max_blocks_per_seq, max_context_len, partition_size,
-        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _dev_ptr(workspace, "workspace"), workspace.nbytes,
         _stream(stream)))
 
 
@@ -296,7 +299,7 @@ def pa_decode_attention_planned(pool, q, k_pool, v_pool, block_tables, scale, ou
         _check_pool_tensor(pool, v_pool, "v_pool"),
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], S,
         max_context_len, float(scale), _dev_ptr(out, "out", dt), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), partition_size, _stream(stream)))
+        workspace.nbytes, partition_size, _stream(stream)))
 
 
 def pa_decode_append_attention(pool, q, k_new, v_new, k_pool, v_pool, block_tables, context_lens,
@@ -321,7 +324,7 @@ def pa_decode_append_attention(pool, q, k_new, v_new, k_pool, v_pool, block_tabl
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
         _dev_ptr(context_lens, "context_lens", torch.int32), S, max_context_len, float(scale),
         _dev_ptr(out, "out", dt), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), partition_size, _stream(stream)))
+        workspace.nbytes, partition_size, _stream(stream)))
 
 
 def pa_decode_append_attention_planned(pool, q, k_new, v_new, k_pool, v_pool, block_tables, scale,
@@ -343,7 +346,7 @@ def pa_decode_append_attention_planned(pool, q, k_new, v_new, k_pool, v_pool, bl
         _check_pool_tensor(pool, v_pool, "v_pool"),
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], S,
         max_context_len, float(scale), _dev_ptr(out, "out", dt), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), partition_size, _stream(stream)))
+        workspace.nbytes, partition_size, _stream(stream)))
 
 
 def pa_find_shared_prefixes(block_tables, context_lens, min_shared_blocks=1, block_size=16):
@@ -402,7 +405,7 @@ def pa_decode_attention_shared_prefix(pool, q, k_pool, v_pool, block_tables, con
         _dev_ptr(context_lens, "context_lens", torch.int32), S, gp[0], gp[1], nm, gp[2], ng,
         groups["max_group_size"], groups["max_shared_blocks"], max_context_len, float(scale),
         _dev_ptr(out, "out", dt), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), partition_size, _stream(stream)))
+        workspace.nbytes, partition_size, _stream(stream)))
 
 
 def pa_prefill_attention(pool, q, k_pool, v_pool, block_tables, context_lens, query_start, scale,
@@ -509,7 +512,7 @@ def pa_decode_attention_mass(pool, q, k_pool, v_pool, block_tables, context_lens
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
         _dev_ptr(context_lens, "context_lens", torch.int32), S, max_context_len, float(scale),
         _dev_ptr(out, "out", dt), m_in, m_out, stride, float(decay),
-        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _dev_ptr(workspace, "workspace"), workspace.nbytes,
         partition_size, _stream(stream)))
 
 
@@ -529,7 +532,7 @@ def pa_decode_attention_mass_planned(pool, q, k_pool, v_pool, block_tables, scal
         _check_pool_tensor(pool, v_pool, "v_pool"),
         _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], S,
         max_context_len, float(scale), _dev_ptr(out, "out", dt), m_in, m_out, stride, float(decay),
-        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _dev_ptr(workspace, "workspace"), workspace.nbytes,
         partition_size, _stream(stream)))
 
 
@@ -570,7 +573,7 @@ def pa_evict_tokens(pool, k_pool, v_pool, block_tables, context_lens, keep_lens,
         _dev_ptr(context_lens, "context_lens", torch.int32), S,
         _dev_ptr(keep_lens, "keep_lens", torch.int32), sinks, recent, ctypes.byref(t_in),
         ctypes.byref(t_out), max_context_len, _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.nbytes, _stream(stream)))
 
 
 def pa_device_errors(stream=None) -> int:

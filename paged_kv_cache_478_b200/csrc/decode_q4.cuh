@@ -26,6 +26,17 @@
 //     largest scale of V among the chunk's tokens, and moves (with a rescale of
 //     the accumulators) only when a P could pass 2^15; it is put at 2^10 then,
 //     so that P is a normal number down to 2^-24 of the largest.
+// What bounds it: the unpacking.  Per 16 tokens of a head (2304 bytes of K and V)
+// a warp issues about 310 instructions, 64 AND, 64 fp16 FMA and 16 matrix ones
+// among them; copies alone run at 6.4 TB/s, the arithmetic on data at hand at 5.7,
+// both together at 5.3 (8 x 32768 tokens x 32 heads: 228 us at full clocks; under
+// sustained load the 1000 W cap takes the SM clock down by a tenth, 244-260 us).
+// 200 requests, 458 MB: 105-109 us; 64 requests x 8 KV heads x 8 query heads, 77 MB:
+// 34 us (plan entry, table and first copies 5 us, six chunks 16, merge 5).  Tried
+// and slower: 16 warps an SM at 128 registers (241 us for the long case), copying
+// warps of their own with four heads a copy (242; with setmaxnreg 275), warps that
+// take single heads by themselves (257), K as 64 + n with the constant taken off
+// the sums (242), the shifts on the multiply pipe (256).
 // ldmatrix reads K rows (token, 16 bytes) as they lie; transposed, it pairs
 // two tokens of V in each register.  The pieces of 8 tokens are 128 contiguous
 // bytes, so both are free of bank conflicts.

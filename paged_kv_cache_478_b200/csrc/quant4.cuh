@@ -18,7 +18,10 @@
 // resolution of its range; the second term of s keeps |z| below 2048, where
 // fp16 holds every whole number.  The error is at most s / 2, and a few
 // hundredths of s more at the upper end where s was rounded down.  n and z are
-// those of exact quotients (q4_quotient).  A group that holds an infinity or NaN, or whose
+// those of exact quotients (q4_quotient).  Measured (32 heads x 128 fp16):
+// append of 16384 tokens 110 us, 1024 blocks to 4 bits 90 us and back 70 us, for
+// 344 MB each (3.1, 3.8 and 4.9 TB/s): bound by instructions, about 13 a value
+// one way and 8 the other.  A group that holds an infinity or NaN, or whose
 // range passes fp32, gets s = NaN and reads back as NaN.
 #pragma once
 

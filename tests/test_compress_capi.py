@@ -121,8 +121,9 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
             return 1
 
     t = torch.zeros(4).as_subclass(Elsewhere)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    pa._torch()
+    monkeypatch.setattr(pa, "_current_device", lambda: 0)
     with pytest.raises(ValueError, match="current CUDA device"):
         pa._dev_ptr(t, "t")
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(pa, "_current_device", lambda: 1)
     assert pa._dev_ptr(t, "t") == t.data_ptr()
