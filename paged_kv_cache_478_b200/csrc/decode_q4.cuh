@@ -109,13 +109,26 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// NH: query heads a lane keeps scores of: 2, or 1 where G is 1.
-template <typename T, int D, int NH, bool MASS>
+// d += a * b for one m16n8k32 tile, a of unsigned bytes, b of signed ones, 32-bit sums.
+__device__ __forceinline__ void mma16832_u8s8(int* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+constexpr uint32_t kNibbles = 0x0f0f0f0fu;
+
+// NH: query heads a lane keeps scores of: 2, or 1 where G is 1.  I8 (one or two
+// query heads): the scores by byte products, the queries' digits in the columns.
+template <typename T, int D, int NH, bool I8, bool MASS>
 __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, int heads_per_item) {
   using Cfg = Q4Config<T, D>;
   constexpr int TILE = Cfg::TILE, NSTAGE = Cfg::NSTAGE;
   constexpr int PIECES = D / 32, GROUPS = D / 64;
   constexpr int CB = kQ4ChunkBlocks;
+  // the softmax reference: P stays below 2^(y - ref + 1); it moves beyond kMove, to kPut
+  constexpr float kMove = 14.f, kPut = 10.f;
 
   extern __shared__ __align__(128) uint8_t q4_smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + Cfg::WARPS * NSTAGE * Cfg::STAGE_BYTES);
@@ -183,7 +196,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     const int chunks = (nblk + CB - 1) / CB;
     const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
 
-    float ref[NH], l_run[NH];  // of query heads 2 j and 2 j + 1; l_run over this lane's tokens
+    // of query heads 2 j + e (I8: heads e, the same in the quad's lanes); l_run over this lane's tokens
+    float ref[NH], l_run[NH];
 #pragma unroll
     for (int e = 0; e < NH; ++e) ref[e] = -INFINITY, l_run[e] = 0.f;
     float o[PIECES][2][4];
@@ -218,16 +232,18 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
       const uint32_t k0 = fills;
       for (int i = 0; i < NSTAGE && i < c_n; ++i) issue(k0 + i, c_lo + i);
 
-      // Q fragments (rows >= G are zero), scaled by 2^qe so that the row's
-      // largest value lies in [2^14, 2^15)
-      uint32_t qb[PIECES][4];  // two k-steps of (b0, b1): head r, dimensions 32 c + 8 j .. + 7
-      float kq[NH];            // raw scores to log2 units, positive: a negative scale turns Q
+      // Q fragments, column r, dimensions 32 c + 8 j .. + 7: head r (I8: digit r / 2 of head r % 2); columns
+      // past G are zero
+      uint32_t qb[PIECES][I8 ? 2 : 4];
+      float kq[NH];          // scores to log2 units (I8: of this lane's digit)
+      float qs[GROUPS][NH];  // I8: sum of a group's queries in this lane's digit
       {
+        const int q_head = I8 ? (r & 1) : r;
         float qf[PIECES][8], top = 0.f;
 #pragma unroll
         for (int c = 0; c < PIECES; ++c) {
-          if (r < G) {
-            load8(static_cast<const T*>(a.q) + (sh0 + r) * D + 32 * c + 8 * j, qf[c]);
+          if (q_head < G) {
+            load8(static_cast<const T*>(a.q) + (sh0 + q_head) * D + 32 * c + 8 * j, qf[c]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) qf[c][e] = 0.f;
@@ -238,18 +254,58 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
         const int ex = (int)(__float_as_uint(top) >> 23);  // biased exponent; 255: infinity or NaN
-        const int qe = ex == 255 ? 0 : min(14 + 127 - ex, 100);
-        const float f = copysignf(__uint_as_float((uint32_t)(qe + 127) << 23), a.scale_log2);
-        // 2^(10 - qe); never zero, so that a masked score stays -infinity when the scale is 0
-        const float mine_kq = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + 10 - qe) << 23),
-                                    1.17549435e-38f);
+        if constexpr (I8) {
+          // as whole numbers, the row's largest in [2^21, 2^22), of three signed base-256 digits; column r
+          // is digit r / 2, the leading one first, of head r % 2
+          const int term = r >> 1;
+          const int qe = ex == 255 ? 0 : min(21 + 127 - ex, 126);
+          const float f = __uint_as_float((uint32_t)(qe + 127) << 23);
+          float probe = 0.f;  // NaN once a query is NaN or infinite
+          auto digit = [&](float x, int* sum) {
+            probe = fmaf(x, 0.f, probe);
+            const int v = __float2int_rn(x * f);
+            const int d0 = (int)(int8_t)v, v1 = (v - d0) >> 8;
+            const int d1 = (int)(int8_t)v1, d2 = (v1 - d1) >> 8;
+            const int d = term == 0 ? d2 : term == 1 ? d1 : term == 2 ? d0 : 0;
+            *sum += d;
+            return (uint32_t)d & 0xffu;
+          };
 #pragma unroll
-        for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 8 * j + 4 * e);
+          for (int gr = 0; gr < GROUPS; ++gr) {
+            int sum = 0;
 #pragma unroll
-        for (int c = 0; c < PIECES; ++c)
+            for (int c = 2 * gr; c < 2 * gr + 2; ++c) {
+              qb[c][0] = qb[c][1] = 0u;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)  // pairs as the nibbles lie in a register: (0, 4), (1, 5), ...
-            qb[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
+              for (int e = 0; e < 8; ++e)  // as the numbers lie in a register: the even ones, then the odd ones
+                qb[c][e & 1] |= digit(qf[c][e], &sum) << (8 * (e / 2));
+            }
+            sum += __shfl_xor_sync(kFullMask, sum, 1);
+            sum += __shfl_xor_sync(kFullMask, sum, 2);
+#pragma unroll
+            for (int e = 0; e < NH; ++e) qs[gr][e] = (float)__shfl_sync(kFullMask, sum, 4 * (2 * j + e));
+          }
+          probe += __shfl_xor_sync(kFullMask, probe, 1);
+          probe += __shfl_xor_sync(kFullMask, probe, 2);
+          const float mine_kq = __uint_as_float((uint32_t)(127 - qe) << 23) + probe;
+          const float kj = a.scale_log2 * __uint_as_float((uint32_t)(127 + 16 - 8 * j) << 23);  // the digit's weight
+#pragma unroll
+          for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 4 * e) * kj;
+        } else {
+          // scaled by 2^qe so that the row's largest value lies in [2^14, 2^15); a negative scale turns Q
+          const int qe = ex == 255 ? 0 : min(14 + 127 - ex, 100);
+          const float f = copysignf(__uint_as_float((uint32_t)(qe + 127) << 23), a.scale_log2);
+          // 2^(10 - qe); never zero, so that a masked score stays -infinity when the scale is 0
+          const float mine_kq = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + 10 - qe) << 23),
+                                      1.17549435e-38f);
+#pragma unroll
+          for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 8 * j + 4 * e);
+#pragma unroll
+          for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // pairs as the nibbles lie in a register: (0, 4), (1, 5), ...
+              qb[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
+        }
       }
 
       int i = 0;
@@ -274,7 +330,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           __syncwarp();
         }
 
-        // ---- raw scores of the chunk: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e
+        // ---- scores of the chunk, raw or (I8) in log2 units: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e (e)
         float x[CB][2][NH];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
@@ -290,31 +346,63 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             kw[0][0] = w[0], kw[0][1] = w[1], kw[1][0] = w[2], kw[1][1] = w[3];
           }
           const uint8_t* words = kt + b * TILE + q4_words_off(D) + r * 4;
+          if constexpr (I8) {
 #pragma unroll
-          for (int gr = 0; gr < GROUPS; ++gr) {
-            uint32_t word[2];
-            __half2 nz[2];  // -z 2^-10 of the two tokens, in both halves
+            for (int gr = 0; gr < GROUPS; ++gr) {
+              int c[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              word[nt] = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
-              nz[nt] = __hmul2(as_half2(__byte_perm(word[nt], word[nt], 0x1010)), as_half2(kMinus2m10));
-            }
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+              for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
+                const uint32_t w0 = kw[0][pc], w1 = kw[1][pc];
+                const uint32_t am[4] = {w0 & kNibbles, w1 & kNibbles, (w0 >> 4) & kNibbles, (w1 >> 4) & kNibbles};
+                mma16832_u8s8(c, am, qb[pc][0], qb[pc][1]);
+              }
 #pragma unroll
-            for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
-              const uint32_t w0 = kw[0][pc], w1 = kw[1][pc], u0 = w0 >> 8, u1 = w1 >> 8;
-              const uint32_t a0[4] = {q4_even(w0, nz[0]), q4_even(w1, nz[1]), q4_odd(w0, nz[0]), q4_odd(w1, nz[1])};
-              const uint32_t a1[4] = {q4_even(u0, nz[0]), q4_even(u1, nz[1]), q4_odd(u0, nz[0]), q4_odd(u1, nz[1])};
-              mma16816<__half>(c, a0, qb[pc][0], qb[pc][1]);
-              mma16816<__half>(c, a1, qb[pc][2], qb[pc][3]);
+              for (int nt = 0; nt < 2; ++nt) {
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
+                const float sc = q4_scale(word), z = q4_zero(word);
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                  const float d = fmaf(-z, qs[gr][e], (float)c[2 * nt + e]);
+                  x[b][nt][e] = gr == 0 ? sc * d : fmaf(sc, d, x[b][nt][e]);
+                }
+              }
             }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-              for (int e = 0; e < NH; ++e) {
-                const float sc = q4_scale(word[nt]);
-                x[b][nt][e] = gr == 0 ? sc * c[2 * nt + e] : fmaf(sc, c[2 * nt + e], x[b][nt][e]);
+              for (int e = 0; e < NH; ++e) {  // the digits, over the quad's lanes
+                float v = x[b][nt][e] * kq[e];
+                v += __shfl_xor_sync(kFullMask, v, 1);
+                v += __shfl_xor_sync(kFullMask, v, 2);
+                x[b][nt][e] = v;
               }
+          } else {
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) {
+              uint32_t word[2];
+              __half2 nz[2];  // -z 2^-10 of the two tokens, in both halves
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                word[nt] = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
+                nz[nt] = __hmul2(as_half2(__byte_perm(word[nt], word[nt], 0x1010)), as_half2(kMinus2m10));
+              }
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int pc = 2 * gr; pc < 2 * gr + 2; ++pc) {
+                const uint32_t w0 = kw[0][pc], w1 = kw[1][pc], u0 = w0 >> 8, u1 = w1 >> 8;
+                const uint32_t a0[4] = {q4_even(w0, nz[0]), q4_even(w1, nz[1]), q4_odd(w0, nz[0]), q4_odd(w1, nz[1])};
+                const uint32_t a1[4] = {q4_even(u0, nz[0]), q4_even(u1, nz[1]), q4_odd(u0, nz[0]), q4_odd(u1, nz[1])};
+                mma16816<__half>(c, a0, qb[pc][0], qb[pc][1]);
+                mma16816<__half>(c, a1, qb[pc][2], qb[pc][3]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                  const float sc = q4_scale(word[nt]);
+                  x[b][nt][e] = gr == 0 ? sc * c[2 * nt + e] : fmaf(sc, c[2 * nt + e], x[b][nt][e]);
+                }
+            }
           }
         }
         if (valid < kQ4Chunk) {
@@ -330,13 +418,14 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         if constexpr (MASS) {
 #pragma unroll
           for (int e = 0; e < NH; ++e) {
-            if (2 * j + e >= G) continue;
-            float* dst = a.scores + (sh0 + 2 * j + e) * a.score_stride + tok0 + (c_lo + i) * kQ4Chunk + r;
+            if (!I8 && 2 * j + e >= G) continue;
+            float* dst = a.scores + (sh0 + (I8 ? e : 2 * j + e)) * a.score_stride + tok0 + (c_lo + i) * kQ4Chunk + r;
 #pragma unroll
             for (int b = 0; b < CB; ++b)
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt)
-                if (b * 16 + nt * 8 + r < valid) dst[b * 16 + nt * 8] = x[b][nt][e] * kq[e];
+              for (int nt = 0; nt < 2; ++nt)  // I8: the quad's lanes hold the same, and store a block each
+                if ((!I8 || (b & 3) == j) && b * 16 + nt * 8 + r < valid)
+                  dst[b * 16 + nt * 8] = I8 ? x[b][nt][e] : x[b][nt][e] * kq[e];
           }
         }
 
@@ -366,16 +455,16 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         bool move = false;
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
-          y[e] = fmaf(mx[e], kq[e], ev);
-          move |= y[e] > ref[e] + 14.f;
+          y[e] = I8 ? mx[e] + ev : fmaf(mx[e], kq[e], ev);
+          move |= y[e] > ref[e] + kMove;
         }
         if (__any_sync(kFullMask, move)) {
           float alpha[2] = {1.f, 1.f};
 #pragma unroll
           for (int e = 0; e < NH; ++e)
-            if (y[e] > ref[e] + 14.f) {
-              alpha[e] = ex2(ref[e] - (y[e] - 10.f));  // 0 on the first move
-              ref[e] = y[e] - 10.f;
+            if (y[e] > ref[e] + kMove) {
+              alpha[e] = ex2(ref[e] - (y[e] - kPut));  // 0 on the first move
+              ref[e] = y[e] - kPut;
               l_run[e] *= alpha[e];
             }
 #pragma unroll
@@ -383,7 +472,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[c][m][e] *= alpha[e & 1];
+              for (int e = 0; e < 4; ++e) o[c][m][e] *= alpha[NH == 2 ? e & 1 : 0];
         }
         float mb[NH];
 #pragma unroll
@@ -397,19 +486,31 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < NH; ++e) {
-              w[nt][e] = ex2(fmaf(x[b][nt][e], kq[e], mb[e]));
+              w[nt][e] = ex2(I8 ? x[b][nt][e] + mb[e] : fmaf(x[b][nt][e], kq[e], mb[e]));
               l_run[e] += w[nt][e];
             }
           const uint32_t tile = smem_addr(vt + b * TILE);
           const uint8_t* words = vt + b * TILE + q4_words_off(D);
+          uint32_t pc[2];  // I8: the quad's lanes take the groups' P in turn, each in columns of its own
+          if constexpr (I8) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + (GROUPS == 2 ? (j & 1) * 64 : 0) + nt * 32 + r * 4));
+              pc[nt] = movmatrix(pack_half(w[nt][0] * sc, NH == 2 ? w[nt][NH - 1] * sc : 0.f));
+            }
+          }
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
             uint32_t pb[2];
             __half2 nz[2];  // -z 2^-10 of tokens 2 j and 2 j + 1
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
-              pb[nt] = movmatrix(pack_half(w[nt][0] * sc, NH == 2 ? w[nt][NH - 1] * sc : 0.f));
+              if constexpr (I8) {
+                pb[nt] = pc[nt];
+              } else {
+                const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
+                pb[nt] = movmatrix(pack_half(w[nt][0] * sc, w[nt][NH - 1] * sc));
+              }
               const uint2 two = *reinterpret_cast<const uint2*>(words + gr * 64 + nt * 32 + j * 8);
               nz[nt] = __hmul2(as_half2(__byte_perm(two.x, two.y, 0x5410)), as_half2(kMinus2m10));
             }
@@ -484,30 +585,61 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[c][m][e] = o[c][m][e] * sa[e & 1] + xs[((c * 2 + m) * 4 + e) * 32 + lane] * sb[e & 1];
+              o[c][m][e] = o[c][m][e] * sa[NH == 2 ? e & 1 : 0] +
+                           xs[((c * 2 + m) * 4 + e) * 32 + lane] * sb[NH == 2 ? e & 1 : 0];
       }
       if (wph > 1) fence_proxy_async_shared();  // the other warps' rings are refilled after the loop's barrier
-      // this lane holds dimensions 32 c + 4 r .. + 3 of heads 2 j and 2 j + 1
+      if constexpr (I8) {
+        // the lanes of a quad hold the same heads; with two groups, even lanes the first one's dimensions, odd
+        // ones the second's: each writes a piece
+        const int piece = GROUPS == 2 ? 2 * (j & 1) + (j >> 1) : j;
 #pragma unroll
-      for (int e = 0; e < NH; ++e) {
-        const int h = 2 * j + e;
-        if (h >= G) continue;
-        // the accumulators hold 2^-10 of their sums
-        const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
+        for (int e = 0; e < NH; ++e) {
+          // the accumulators hold 2^-10 of their sums
+          const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
+          float v[4];
 #pragma unroll
-        for (int c = 0; c < PIECES; ++c) {
-          const float v[4] = {o[c][0][e] * inv, o[c][0][2 + e] * inv, o[c][1][e] * inv, o[c][1][2 + e] * inv};
-          if (!split) {
-            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
-                make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
-          } else {
-            *reinterpret_cast<float4*>(a.part_acc + ((sh0 + h) * a.max_parts + p) * D + 32 * c + 4 * r) =
-                make_float4(v[0], v[1], v[2], v[3]);
+          for (int c = 0; c < PIECES; ++c)
+            if (c == piece) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = o[c][k >> 1][2 * (k & 1) + e] * inv;
+            }
+          if (piece < PIECES) {
+            if (!split)
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + e) * D + 32 * piece + 4 * r) =
+                  make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
+            else
+              *reinterpret_cast<float4*>(a.part_acc + ((sh0 + e) * a.max_parts + p) * D + 32 * piece + 4 * r) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+          }
+          if (lane == 0) {
+            if (split) a.part_ml[(sh0 + e) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
+            else if (MASS) a.lse[sh0 + e] = ref[e] + log2f(l_run[e]);
           }
         }
-        if (r == 0) {
-          if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
-          else if (MASS) a.lse[sh0 + h] = ref[e] + log2f(l_run[e]);
+      } else {
+        // this lane holds dimensions 32 c + 4 r .. + 3 of heads 2 j and 2 j + 1
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          const int h = 2 * j + e;
+          if (h >= G) continue;
+          // the accumulators hold 2^-10 of their sums
+          const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
+#pragma unroll
+          for (int c = 0; c < PIECES; ++c) {
+            const float v[4] = {o[c][0][e] * inv, o[c][0][2 + e] * inv, o[c][1][e] * inv, o[c][1][2 + e] * inv};
+            if (!split) {
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
+                  make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
+            } else {
+              *reinterpret_cast<float4*>(a.part_acc + ((sh0 + h) * a.max_parts + p) * D + 32 * c + 4 * r) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            }
+          }
+          if (r == 0) {
+            if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
+            else if (MASS) a.lse[sh0 + h] = ref[e] + log2f(l_run[e]);
+          }
         }
       }
     }
