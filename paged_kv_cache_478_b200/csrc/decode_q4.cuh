@@ -5,38 +5,51 @@
 // head through its own ring of bulk copies, 64 tokens (4 blocks) a stage, and
 // serves all G query heads of it.
 //
-// The products run on the tensor cores without an integer conversion of the
-// held numbers: 4 bits n in the low bits of an fp16 word ARE the number n 2^-24
-// (a subnormal), and bits 4-7 are n 2^-20, so one AND and one fp16 FMA make (n - z)
-// 2^-10 of two numbers, exactly (|n - z| is below 2048).  Feeding the subnormals
-// themselves to the matrix instructions would save the FMA, but those line up a
-// sum by the exponents its operands are written with: subnormals cost it 6 to 10
-// bits (measured: sums off by 2^-18 of their terms).
-//   scores:  x_t = sum_g s_t,g sum_d q_d (n_t,d - z_t,g), g a group of 64 dimensions.
-//     K is the A operand (16 tokens), Q the B operand (8 columns, G of them
-//     used), scaled by a power of two into fp16's range (exact for fp16 and
-//     bf16 queries).  A lane gets the scores of tokens lane / 4 and lane / 4 + 8
-//     of each block and of heads 2 (lane % 4) and the next, so that one word a
-//     token and group gives both its zero point and its scale.
+// The products run on the tensor cores, the held numbers n in one of two forms.
+//   fp16: 4 bits n in the low bits of an fp16 word ARE the number n 2^-24 (a
+//     subnormal), and bits 4-7 are n 2^-20, so one AND and one fp16 FMA make
+//     (n - z) 2^-10 of two numbers, exactly (|n - z| is below 2048).  Feeding the
+//     subnormals themselves to the matrix instructions would save the FMA, but
+//     those line up a sum by the exponents its operands are written with:
+//     subnormals cost it 6 to 10 bits (measured: sums off by 2^-18 of their terms).
+//   bytes: one AND, and for the odd numbers a shift, make four numbers.
+//
+//   scores:  x_t = sum_g s_t,g (sum_d q_d n_t,d - z_t,g sum_d q_d), g a group of 64
+//     dimensions.  K is the A operand (16 tokens), Q the B operand (8 columns).
+//     One or two query heads: byte products with 32-bit integer sums.  Q becomes
+//     whole numbers, the row's largest in [2^21, 2^22) (off by at most 2^-22 of it;
+//     exact for what is not below 2^-11 of the largest, bf16 2^-14), of three signed
+//     base-256 digits, each in a column of its own; the sums are exact, and the quad's
+//     lanes, which hold a digit each, add their shares in fp32.
+//     Four or eight heads need the columns: fp16, Q scaled by a power of two into
+//     its range, fp32 sums.  A lane gets the scores of tokens lane / 4 and lane / 4 + 8
+//     of each block and of heads 2 (lane % 4) and the next.
+//     In both, one word a token and group gives its zero point and its scale.
 //   values:  o_d = sum_t P_t,g (n_t,d - z_t,g),  P_t,g = w_t s_t,g.
-//     V^T is the A operand; P, rounded to fp16 once (2^-11) and transposed 8 x 8
-//     by movmatrix, the B operand, so its accumulators belong to the same two
-//     heads as the lane's softmax state.
+//     V^T is the A operand in fp16; P, rounded to fp16 once (2^-11) and transposed
+//     8 x 8 by movmatrix, the B operand, so its accumulators belong to the same two
+//     heads as the lane's softmax state.  With one or two heads the quad's lanes hold the
+//     same weights, and even lanes take the first group's scale, odd ones the second's:
+//     one movmatrix makes both groups' operands, and either group's product has
+//     its sums in columns of its own.
 //   P stays within fp16: the softmax reference follows x_t + log2 of the
 //     largest scale of V among the chunk's tokens, and moves (with a rescale of
 //     the accumulators) only when a P could pass 2^15; it is put at 2^10 then,
 //     so that P is a normal number down to 2^-24 of the largest.
 // What bounds it: the unpacking.  Per 16 tokens of a head (2304 bytes of K and V)
-// a warp issues about 310 instructions, 64 AND, 64 fp16 FMA and 16 matrix ones
-// among them; copies alone run at 6.4 TB/s, the arithmetic on data at hand at 5.7,
-// both together at 5.3 (8 x 32768 tokens x 32 heads: 228 us at full clocks; under
-// sustained load the 1000 W cap takes the SM clock down by a tenth, 244-260 us).
-// 200 requests, 458 MB: 105-109 us; 64 requests x 8 KV heads x 8 query heads, 77 MB:
-// 34 us (plan entry, table and first copies 5 us, six chunks 16, merge 5).  Tried
-// and slower: 16 warps an SM at 128 registers (241 us for the long case), copying
-// warps of their own with four heads a copy (242; with setmaxnreg 275), warps that
-// take single heads by themselves (257), K as 64 + n with the constant taken off
-// the sums (242), the shifts on the multiply pipe (256).
+// a warp issued about 310 instructions in fp16, 64 AND, 64 fp16 FMA and 16 matrix ones
+// among them (four or eight heads; with fewer, K's half of that is 16 AND, 16
+// shifts and 4 matrix ones).  One head a KV head, before and now: 200 requests, 458 MB,
+// 109 and 98 us; 8 x 32768 tokens x 32 heads 228 and 207 us (5.85 TB/s; copies alone run at 6.4).
+// Under sustained load the 1000 W cap takes the SM clock down by a tenth: 101 and 238 us.
+// 64 requests x 8 KV heads x 8 query heads, 77 MB: 34 us (plan entry, table and first
+// copies 5 us, six chunks 16, merge 5).
+// Tried on the fp16 form and slower (the long case): 16 warps an SM at 128 registers
+// (241 us), copying warps of their own with four heads a copy (242; with setmaxnreg
+// 275), warps that take single heads by themselves (257), K as 64 + n with the constant
+// taken off the sums (242), the shifts on the multiply pipe (256), e4m3 operands (285;
+// mma.sync turns them into fp16 first).  V by byte products would need its scales
+// bounded: P as a whole number keeps 23 bits below the largest scale that may come.
 // ldmatrix reads K rows (token, 16 bytes) as they lie; transposed, it pairs
 // two tokens of V in each register.  The pieces of 8 tokens are 128 contiguous
 // bytes, so both are free of bank conflicts.
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     const int chunks = (nblk + CB - 1) / CB;
     const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
 
-    // of query heads 2 j + e (I8: heads e, the same in the quad's lanes); l_run over this lane's tokens
+    // of query heads 2 j + e (I8: heads e, the same in the quad's lanes); l_run is over this lane's tokens
     float ref[NH], l_run[NH];
 #pragma unroll
     for (int e = 0; e < NH; ++e) ref[e] = -INFINITY, l_run[e] = 0.f;
@@ -495,7 +508,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           if constexpr (I8) {
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + (GROUPS == 2 ? (j & 1) * 64 : 0) + nt * 32 + r * 4));
+              const float sc = q4_scale(
+                  *reinterpret_cast<const uint32_t*>(words + (GROUPS == 2 ? (j & 1) * 64 : 0) + nt * 32 + r * 4));
               pc[nt] = movmatrix(pack_half(w[nt][0] * sc, NH == 2 ? w[nt][NH - 1] * sc : 0.f));
             }
           }

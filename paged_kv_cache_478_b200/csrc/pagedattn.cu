@@ -496,9 +496,9 @@ int auto_partition(int num_seqs, int head_groups, int max_context_len, int slots
 // results and merge: about 6 us) weighs four times as much as on 16-bit pools,
 // so partitions are long where the batch allows it: about 3.6 times as many
 // tokens of the longest sequences as the slots, at most 2048 a partition
-// (200 requests x 32 heads up to 2048: 108 us at 2048, 120 at 512, 141 at 256;
+// (200 requests x 32 heads up to 2048: 98 us at 2048, 103 at 1024, 112 at 512;
 // 200 x 8 KV heads: 46 us at 512, 54 at 256 and at 768, 86 at 1536, where the
-// longest items outlast the rest; 8 x 32768 x 32 heads: 227 at 2048, 248 at 512).
+// longest items outlast the rest; 8 x 32768 x 32 heads: 207 at 2048, 229 at 512).
 // A small batch gets one item per slot, the mean length taken as half the
 // longest, as long as that keeps partitions within 512 (64 x 8 KV heads up to
 // 2048: 34 us at 384, one item per slot; 41 at 256, 39 at 512).  Whole chunks.

@@ -6,6 +6,8 @@ Tolerance of the attention, from the arithmetic (D dimensions, N tokens):
   numerator weight, times its scale, is rounded once to fp16: 2^-11 of it, or
   2^-25 of the largest where it is subnormal.  A score is an fp32 sum of D products
   and of the zero point's term, off by at most D 2^-24 scale sum |q| s (n + |z|) =: e;
+  (with one or two query heads the products' sums are whole numbers, exact, of queries
+  off by at most 2^-22 of the row's largest: for the rows drawn here below e);
   with the exponential's own 2^-22 that moves a weight by a factor of 1 + e + 2^-22,
   in the numerator and in the denominator.  The numerator is an fp32 sum of N
   products, each of which enters a partial sum by rounding or chopping, at most 2^-23 of it:
