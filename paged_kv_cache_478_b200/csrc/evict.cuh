@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_select_kernel(EvictArg
     sh.need = keep;
     sh.done = -1;
   }
+  __syncthreads();  // keep == 0 goes past the loop's barriers
   // the keep-th largest key, from its first digit on; a pass whose whole bin stays is the last
   int pass = 0, shift = 0;
   for (; pass < 3 && keep > 0; ++pass) {

@@ -239,6 +239,27 @@ def test_evict_of_a_long_sequence():
         assert np.array_equal(rows_of(k, 64), want)
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+def test_evict_of_everything(inplace):
+    """keep 0: no pass of the selection runs, and nothing moves."""
+    rng = np.random.default_rng(81)
+    lengths = [5000, 1, 0, 33, 17000] * 20  # clusters of 8 CTAs each
+    c = any_case_bytes(rng, lengths, 1, 64, "f16")
+    stride = c["tables"].shape[1] * 16
+    state = evict_state(rng, lengths, [0] * len(lengths), stride)
+    for sinks, recent in ((0, 0), (4, 64)):
+        k, v = c["k"].clone(), c["v"].clone()
+        after = run_evict(c, [0] * len(lengths), sinks, recent, state, inplace, k, v)
+        assert pa.pa_device_errors() == 0
+        got = after["mass"].cpu().numpy()
+        for s, L in enumerate(lengths):
+            h, nxt = state[2][s]
+            assert (got[s, :L] == 0).all()
+            assert after["history"][s].tolist() == ([0, nxt + L - h] if L else [h, nxt])
+        assert torch.equal(k.view(torch.int16), c["k"].view(torch.int16))
+        assert torch.equal(v.view(torch.int16), c["v"].view(torch.int16))
+
+
 def test_evict_reports_bad_lengths_and_blocks():
     rng = np.random.default_rng(9)
     c = any_case_bytes(rng, [40, 40, 40], 2, 64, "f16")
