@@ -140,7 +140,8 @@ pa_status pa_pool_set_query_heads(pa_pool* pool, int32_t num_q_heads);
  * k_pool[slot / bs][h][slot % bs][:] = k_new[t][h][:] for every head, the
  * same for V (7minutos.es section 2: the new token goes into the tail page).
  * Bit copy (4-bit pools: quantised).  A negative slot is skipped; a slot >= num_blocks * block_size
- * sets PA_DEVERR_SLOT and is skipped.  num_tokens == 0 is a no-op.
+ * sets PA_DEVERR_SLOT and is skipped.  Two tokens of one call must not name the
+ * same slot.  num_tokens == 0 is a no-op.
  */
 pa_status pa_reshape_and_cache(const pa_pool* pool, const void* k_new, const void* v_new,
                                const int32_t* slot_mapping, int32_t num_tokens, void* k_pool,
@@ -461,7 +462,7 @@ typedef struct pa_track {
  * keep_lens: device int32 [num_seqs]; a negative one sets
  * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole.  The blocks of every
  * evicted sequence must be private to it (copy them on write first).  All
- * pool types.  At most 65535 sequences.
+ * pool types.  At most 65535 sequences and contexts of 2^30 tokens.
  * workspace: pa_evict_workspace_bytes().
  */
 pa_status pa_evict_workspace_bytes(const pa_pool* pool, int32_t num_seqs, int32_t max_blocks_per_seq,

@@ -459,6 +459,8 @@ struct MassLayout {
   int64_t stride = 0;  // tokens between query heads
 };
 
+constexpr int kMaxMassSeqs = 65535;  // sequences are a grid's second dimension
+
 MassLayout mass_layout(const pa_pool* pool, int64_t S, int maxL) {
   MassLayout m;
   const int64_t rows = S * pool->heads * pool->q_per_kv;
@@ -702,6 +704,7 @@ pa_status pa_decode_mass_workspace_bytes(const pa_pool* pool, int32_t num_seqs,
   pa_status st = pa_decode_workspace_bytes(pool, num_seqs, max_blocks_per_seq, max_context_len,
                                            partition_size, &base);
   if (st != PA_OK) return st;
+  if (num_seqs > kMaxMassSeqs) return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
   *bytes = base + mass_layout(pool, num_seqs,
                               resolve_max_context(pool, max_blocks_per_seq, max_context_len))
                       .total;
@@ -1299,9 +1302,8 @@ pa_status check_mass(const float* mass_out, int64_t stride, float decay, int max
 
 pa_status launch_mass(const DecodeArgs& a, const MassArgs& m, cudaStream_t s) {
   if (a.max_context_len == 0) return PA_OK;
-  if (a.num_seqs > 65535)
-    return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
-  const dim3 grid((unsigned)((a.max_context_len + kMassTokens - 1) / kMassTokens), (unsigned)a.num_seqs);
+  const int64_t ctas = ((int64_t)a.max_context_len + kMassTokens - 1) / kMassTokens;
+  const dim3 grid((unsigned)ctas, (unsigned)a.num_seqs);
   const cudaError_t e = launch_dependent(mass_kernel, grid, kMassWarps * 32, s, a, m);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "mass launch");
 }
@@ -1315,7 +1317,7 @@ pa_status decode_mass(const pa_pool* pool, const void* q, const void* k_pool, co
                       size_t workspace_bytes, int32_t partition_size, cudaStream_t s) {
   if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "decode mass: num_seqs < 0");
   if (num_seqs == 0) return check_pool(pool);
-  if (num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
+  if (num_seqs > kMaxMassSeqs) return fail(PA_ERR_INVALID_ARG, "decode mass: more than 65535 sequences");
   pa_status st = check_run_pointers(q, k_pool, v_pool, block_tables, out, scale);
   if (st != PA_OK) return st;
   if (!planned && !context_lens) return fail(PA_ERR_INVALID_ARG, "decode mass: context_lens is null");
@@ -1353,6 +1355,15 @@ EvictLayout evict_layout(int64_t S, int maxL) {
   e.moves = align256(S * sizeof(int4));
   e.total = align256(e.moves + S * e.cap * 8);
   return e;
+}
+
+// What the kernels index in 32 bits, with room for a cluster's rounding up.
+pa_status check_evict_sizes(const pa_pool* pool, int32_t num_seqs, int32_t max_blocks_per_seq,
+                            int32_t max_context_len) {
+  if (num_seqs > kMaxMassSeqs) return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: more than 65535 sequences");
+  if (resolve_max_context(pool, max_blocks_per_seq, max_context_len) > (1 << 30))
+    return fail(PA_ERR_UNSUPPORTED, "pa_evict_tokens: contexts of at most 2^30 tokens");
+  return PA_OK;
 }
 
 }  // namespace
@@ -1393,6 +1404,7 @@ pa_status pa_evict_workspace_bytes(const pa_pool* pool, int32_t num_seqs, int32_
   if (!bytes) return fail(PA_ERR_INVALID_ARG, "workspace bytes: bytes is null");
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
     return fail(PA_ERR_INVALID_ARG, "workspace bytes: bad size");
+  if ((st = check_evict_sizes(pool, num_seqs, max_blocks_per_seq, max_context_len)) != PA_OK) return st;
   *bytes = evict_layout(num_seqs, resolve_max_context(pool, max_blocks_per_seq, max_context_len)).total;
   return PA_OK;
 }
@@ -1409,7 +1421,7 @@ pa_status pa_evict_tokens(const pa_pool* pool, void* k_pool, void* v_pool,
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || sinks < 0 || recent < 0)
     return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: bad size");
   if (num_seqs == 0) return PA_OK;
-  if (num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: more than 65535 sequences");
+  if ((st = check_evict_sizes(pool, num_seqs, max_blocks_per_seq, max_context_len)) != PA_OK) return st;
   if (!k_pool || !v_pool || !block_tables || !context_lens || !keep_lens || !in || !out ||
       !in->mass || !in->positions || !in->history || !out->mass || !out->positions || !out->history)
     return fail(PA_ERR_INVALID_ARG, "pa_evict_tokens: null pointer");

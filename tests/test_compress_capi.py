@@ -110,6 +110,20 @@ def test_evict_refusals():
     assert call(S=0) == 0
 
 
+def test_sizes_beyond_the_kernels_indexes_are_refused():
+    lib, p = pa.lib(), pa.pa_pool_create(16, 16, 2, 64, pa.PA_Q4_F16)
+    n = ctypes.c_size_t()
+    ask = lambda pool, S, blocks: lib.pa_evict_workspace_bytes(ctypes.byref(pool), S, blocks, 0, ctypes.byref(n))  # noqa: E731
+    assert ask(p, 65535, 1 << 26) == 0 and n.value >= 65535 * (1 << 29) * 8
+    assert ask(p, 65536, 4) == 1 and ask(p, 1, (1 << 26) + 1) == 2
+    assert lib.pa_decode_mass_workspace_bytes(ctypes.byref(p), 65536, 4, 0, 0, ctypes.byref(n)) == 1
+    t = pa.pa_track(0x2000, 0x3000, 0x4000, 1 << 31)
+    assert lib.pa_evict_tokens(ctypes.byref(p), OK, OK, OK, (1 << 26) + 1, OK, 1, OK, 0, 0, ctypes.byref(t), ctypes.byref(t),
+                               0, OK, 1 << 40, None) == 2
+    with pytest.raises(pa.PagedAttnError):  # slots are 32-bit numbers
+        pa.pa_pool_create(1 << 27, 16, 1, 64, pa.PA_Q4_F16)
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """The launch goes to the current device: a tensor elsewhere is refused before any call."""
     import torch
