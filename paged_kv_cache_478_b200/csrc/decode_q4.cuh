@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             if (ws[e] < 0x7f800000u) big = max(big, ws[e]);  // NaN scales do not count
         }
         big = __reduce_max_sync(kFullMask, big);
-        const float ev = (float)max((int)(big >> 23) - 127, -100);
+        // not below 2^-90 (no scale at all: V is zero): the weights reach 2^(90 + kMove), of which 2^23 add up in fp32
+        const float ev = (float)max((int)(big >> 23) - 127, -90);
         float y[NH];
         bool move = false;
 #pragma unroll

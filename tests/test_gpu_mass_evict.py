@@ -142,6 +142,24 @@ def test_mass_of_a_stale_plan_touches_nothing():
     assert (mass == 2).all() and (out == 7).all()
 
 
+@pytest.mark.parametrize("group", [1, 2, 8])
+def test_mass_over_a_long_cache_of_zeros(group):
+    """K and V all zero (scale 0): every weight is 1 / L, however long the cache.  The softmax sum's
+    logarithm, below 2^7 + 2^7, and its reference are fp32: off by 2^-17 each, a weight by 2^-16."""
+    L, dim = 300001, 64
+    blocks = -(-L // 16)
+    pool = pa.pa_pool_set_query_heads(pa.pa_pool_create(blocks, 16, 1, dim, pa.PA_Q4_BF16), group)
+    k = torch.zeros((blocks, 1, 9 * dim), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    q = torch.ones((1, group, dim), dtype=torch.bfloat16, device="cuda")
+    out, mass = torch.full_like(q, 7), torch.full((1, blocks * 16), -1.0, device="cuda")
+    tables = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+    ws = mass_workspace(pool, 1, blocks)
+    pa.pa_decode_attention_mass(pool, q, k, v, tables, cuda(np.array([L], dtype=np.int32)), 0.125, out, None, mass, ws)
+    assert (out == 0).all() and (mass[0, L:] == -1).all()
+    assert ((mass[0, :L] * L / group - 1).abs() <= 2.0 ** -16).all()
+
+
 # ---- eviction --------------------------------------------------------------------------
 
 def evict_state(rng, lengths, keeps, stride, ties=False):
