@@ -48,8 +48,8 @@
 // (241 us), copying warps of their own with four heads a copy (242; with setmaxnreg
 // 275), warps that take single heads by themselves (257), K as 64 + n with the constant
 // taken off the sums (242), the shifts on the multiply pipe (256), e4m3 operands (285;
-// mma.sync turns them into fp16 first).  V by byte products would need its scales
-// bounded: P as a whole number keeps 23 bits below the largest scale that may come.
+// mma.sync turns them into fp16 first).  V by byte products was left out: the
+// zero points' share, taken off after the sums, would leave their rounding where n - z is 0.
 // ldmatrix reads K rows (token, 16 bytes) as they lie; transposed, it pairs
 // two tokens of V in each register.  The pieces of 8 tokens are 128 contiguous
 // bytes, so both are free of bank conflicts.

@@ -19,8 +19,8 @@
 // fp16 holds every whole number.  The error is at most s / 2, and a few
 // hundredths of s more at the upper end where s was rounded down.  n and z are
 // those of exact quotients (q4_quotient).  Measured (32 heads x 128 fp16):
-// append of 16384 tokens 110 us, 1024 blocks to 4 bits 90 us and back 70 us, for
-// 344 MB each (3.1, 3.8 and 4.9 TB/s): bound by instructions, about 13 a value
+// append of 16384 tokens 98 us, 1024 blocks to 4 bits 80 us and back 70 us, for
+// 344 MB each (3.5, 4.3 and 4.9 TB/s): bound by instructions, about 10 a value
 // one way and 8 the other.  A group that holds an infinity or NaN, or whose
 // range passes fp32, gets s = NaN and reads back as NaN.
 #pragma once
@@ -65,16 +65,15 @@ struct Pair<__nv_bfloat16> {
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: x + kRoundMagic holds round(x) in its low bits
 
 // round(x / s) + kRoundMagic, given inv = 1 / s rounded, halves to even as
-// the exact quotient has them.  x * inv is off by at most 2^-23 of itself.  A
-// quotient of 11 by 8 significant bits below 2048 that is no half differs from
-// one by 2^-9 or by 2^-12 of itself, at any rate by 2^-20 of itself: rounding x *
-// inv to 21 bits (Veltkamp's splitting, by at most 2^-21) puts halves back on
-// their place and moves nothing onto or across one.
+// the exact quotient has them; |x / s| < 2048.  The product with 1.5 2^12 added is
+// rounded to a multiple of 2^-11.  x inv is off by less than 2^-24 of 2048 = 2^-13,
+// so a half comes back to its place.  A quotient of 11 by 8 significant bits that is
+// no half is X / (S 2^t) with X < 2^11 and S < 2^8: where t <= 0 it differs from one by
+// 2^-9, else by 1 / (S 2^t), which is above 2^-12 (half a step) beside 1/2 except
+// for 2047 / 4096, where a step's tie goes to 1/2 and, like itself, to 0.
 __device__ __forceinline__ float q4_quotient(float x, float inv) {
-  const float q = __fmul_rn(x, inv);
-  const float c = __fmul_rn(q, 9.f);
-  const float h = __fsub_rn(c, __fsub_rn(c, q));
-  return __fadd_rn(h, kRoundMagic);
+  constexpr float kSteps = 6144.f;
+  return __fadd_rn(__fmaf_rn(x, inv, kSteps), kRoundMagic - kSteps);
 }
 
 // The largest value of a group and the smallest, negated, as a pair in the
