@@ -921,7 +921,7 @@ pa_status launch_run(const pa_pool* pool, const DecodeArgs& a, const DeviceState
 // the plan's lengths, before the attention of the same call reads it.
 pa_status launch_q4_append_last(const DeviceState& dev, const pa_pool* pool, const DecodeArgs& a,
                                 const void* k_new, const void* v_new, cudaStream_t s) {
-  const int64_t threads = (int64_t)a.num_seqs * pool->heads * (pool->head_dim / 64) * 8;
+  const int64_t threads = (int64_t)a.num_seqs * pool->heads * (pool->head_dim / 64) * 4;
   const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev.num_sms * 8);
   if (pool->dtype == PA_Q4_BF16)
     q4_append_last_kernel<<<grid, 256, 0, s>>>(a, static_cast<const __nv_bfloat16*>(k_new),

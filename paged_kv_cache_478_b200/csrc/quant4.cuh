@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t q4_extent(const uint4& u) {
 // A lane's 8 numbers, the first in the lowest 4 bits, given the group's
 // scale, its reciprocal and zero point.
 template <typename T>
-__device__ __forceinline__ uint32_t q4_numbers(const uint4& u, float s, float inv, float z) {
+__device__ __forceinline__ uint32_t q4_numbers(const uint4& u, float s, float inv, int z) {
   if (!(s > 0.f)) return 0u;  // a group of zeros, or s = NaN
   float x[8];
   Chunk<T>::to_float(u, x);
@@ -104,28 +104,29 @@ __device__ __forceinline__ uint32_t q4_numbers(const uint4& u, float s, float in
   if (s < 1e-36f) {  // 1 / s or a product may leave the normal numbers: divide
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + z, 0.f), 15.f);
+      const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + (float)z, 0.f), 15.f);
       n |= (uint32_t)v << (4 * e);
     }
     return n;
   }
-  const int off = (int)z - __float_as_int(kRoundMagic);
+  const int off = z - __float_as_int(kRoundMagic);
 #pragma unroll
   for (int e = 0; e < 8; ++e)  // clamp(round(x / s) + z, 0, 15)
     n += (uint32_t)__viaddmin_s32_relu(__float_as_int(q4_quotient(x[e], inv)), off, 15) << (4 * e);
   return n;
 }
 
-// Quantise a K and a V group of 64 values, each held by 8 neighbouring lanes,
-// 8 each (all 32 lanes of the warp call).  *kn and *vn are the lane's numbers;
-// *word is the K group's word in lanes 0 .. 3 of the 8 and the V group's in
-// lanes 4 .. 7, which work out one of the two scales each.
+// Quantise two K and two V groups of 64 values (k[u], v[u]), each held by 8
+// neighbouring lanes, 8 each (all 32 lanes of the warp call).  kn[u] and vn[u] are the
+// lane's numbers.  Of the 8 lanes, 2 u and 2 u + 1 work out the scale of K's group u,
+// 4 + 2 u and 5 + 2 u of V's, and *word is its word.
 template <typename T>
-__device__ __forceinline__ void q4_quantise(const uint4& k, const uint4& v, int lane, uint32_t* kn,
+__device__ __forceinline__ void q4_quantise(const uint4* k, const uint4* v, int lane, uint32_t* kn,
                                             uint32_t* vn, uint32_t* word) {
   using V = typename Pair<T>::V;
-  const uint32_t ke = q4_extent<T>(k), ve = q4_extent<T>(v);
-  const uint32_t mine = (lane & 4) ? ve : ke;
+  const uint32_t e0 = q4_extent<T>(k[0]), e1 = q4_extent<T>(k[1]);
+  const uint32_t e2 = q4_extent<T>(v[0]), e3 = q4_extent<T>(v[1]);
+  const uint32_t mine = (lane & 4) ? ((lane & 2) ? e3 : e2) : ((lane & 2) ? e1 : e0);
   const float2 ends = Pair<T>::floats(*reinterpret_cast<const V*>(&mine));
   const float hi = ends.x, lo = -ends.y;
   float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
@@ -133,19 +134,22 @@ __device__ __forceinline__ void q4_quantise(const uint4& k, const uint4& v, int 
   if (big > 1990.f * raw) raw = fmaxf(raw, __fdiv_rn(big, 2000.f));  // the other quotient may be the larger
   float s = __bfloat162float(__float2bfloat16_rn(raw));
   if (!(s < INFINITY)) s = __uint_as_float(0x7fc00000u);
-  float inv = 0.f, z = 0.f;
+  float inv = 0.f;
+  int z = 0;
   if (s >= 1e-36f) {
     inv = __frcp_rn(s);
-    z = __fsub_rn(q4_quotient(-lo, inv), kRoundMagic);
+    z = __float_as_int(q4_quotient(-lo, inv)) - __float_as_int(kRoundMagic);
   } else if (s > 0.f) {
-    z = rintf(__fdiv_rn(-lo, s)) + 0.f;
+    z = (int)rintf(__fdiv_rn(-lo, s));
   }
-  *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__float2half_rn(z));
-  const float s2 = __shfl_xor_sync(kFullMask, s, 4), inv2 = __shfl_xor_sync(kFullMask, inv, 4);
-  const float z2 = __shfl_xor_sync(kFullMask, z, 4);
-  const bool own_v = (lane & 4) != 0;
-  *kn = q4_numbers<T>(k, own_v ? s2 : s, own_v ? inv2 : inv, own_v ? z2 : z);
-  *vn = q4_numbers<T>(v, own_v ? s : s2, own_v ? inv : inv2, own_v ? z : z2);
+  *word = __float_as_uint(s) | (uint32_t)__half_as_ushort(__int2half_rn(z));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int from = (lane & 24) + 2 * i;
+    const float si = __shfl_sync(kFullMask, s, from), ii = __shfl_sync(kFullMask, inv, from);
+    const int zi = __shfl_sync(kFullMask, z, from);
+    (i < 2 ? kn[i & 1] : vn[i & 1]) = q4_numbers<T>(i < 2 ? k[i & 1] : v[i & 1], si, ii, zi);
+  }
 }
 
 // Where the lane's 8 numbers of (row t, group g) go in a tile: lane j of the
@@ -193,18 +197,18 @@ __global__ void __launch_bounds__(256)
       ku[i] = *reinterpret_cast<const uint4*>(k_new + src);
       vu[i] = *reinterpret_cast<const uint4*>(v_new + src);
     }
+    uint32_t kn[U], vn[U], word;
+    q4_quantise<T>(ku, vu, lane, kn, vn, &word);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (slot[i] >= num_slots && h[i] == 0 && g[i] == 0 && j == 0) atomicOr(err, PA_DEVERR_SLOT);
-      uint32_t kn, vn, word;
-      q4_quantise<T>(ku[i], vu[i], lane, &kn, &vn, &word);
       if (slot[i] >= 0 && slot[i] < num_slots) {  // a negative slot is padding
         const int64_t tile = ((int64_t)(slot[i] >> 4) * heads + h[i]) * q4_tile_bytes(D);
         const int r = slot[i] & 15;
-        *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g[i], j, r)) = kn;
-        *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g[i], j, r)) = vn;
-        if ((j & 3) == 0)
-          *reinterpret_cast<uint32_t*>((j == 0 ? k_pool : v_pool) + tile + q4_words_off(D) + (g[i] * 16 + r) * 4) = word;
+        *reinterpret_cast<uint32_t*>(k_pool + tile + q4_data_off(g[i], j, r)) = kn[i];
+        *reinterpret_cast<uint32_t*>(v_pool + tile + q4_data_off(g[i], j, r)) = vn[i];
+        if ((j & 3) == 2 * i)
+          *reinterpret_cast<uint32_t*>((j < 4 ? k_pool : v_pool) + tile + q4_words_off(D) + (g[i] * 16 + r) * 4) = word;
       }
     }
   }
@@ -220,39 +224,49 @@ __global__ void __launch_bounds__(256)
   const int groups = D / 64;
   const int64_t total = (int64_t)a.num_seqs * a.heads * groups;
   const int64_t cap = min((int64_t)a.max_context_len, (int64_t)a.max_blocks_per_seq * kBlock);
-  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 < total;
+  constexpr int U = 2;
+  for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w * 4 * U < total;
        w += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t u = w * 4 + (lane >> 3);
-    const bool live = u < total;
-    const int64_t row = live ? u >> (groups - 1) : 0;  // sequence * heads + head
-    const int g = live ? (int)(u - row * groups) : 0;
-    const int s = (int)q4_div(row, a.heads);
-    const int h = (int)(row - (int64_t)s * a.heads);
-    const int L = live ? a.lens[s] : 0;
-    bool write = L > 0 && L <= cap;
-    int32_t b = 0;
-    if (write) {
-      b = a.block_tables[(int64_t)s * a.max_blocks_per_seq + (L - 1) / kBlock];
-      write = b >= 0 && b < a.num_blocks;  // the decode launch reports a bad one
+    uint4 ku[U], vu[U];
+    bool write[U];
+    int64_t tile[U];
+    int g[U], r[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t u = (w * U + i) * 4 + (lane >> 3);
+      const bool live = u < total;
+      const int64_t row = live ? u >> (groups - 1) : 0;  // sequence * heads + head
+      g[i] = live ? (int)(u - row * groups) : 0;
+      const int s = (int)q4_div(row, a.heads);
+      const int h = (int)(row - (int64_t)s * a.heads);
+      const int L = live ? a.lens[s] : 0;
+      write[i] = L > 0 && L <= cap;
+      int32_t b = 0;
+      if (write[i]) {
+        b = a.block_tables[(int64_t)s * a.max_blocks_per_seq + (L - 1) / kBlock];
+        write[i] = b >= 0 && b < a.num_blocks;  // the decode launch reports a bad one
+      }
+      ku[i] = vu[i] = make_uint4(0, 0, 0, 0);
+      if (write[i]) {
+        const int64_t src = row * D + g[i] * 64 + j * 8;
+        ku[i] = *reinterpret_cast<const uint4*>(k_new + src);
+        vu[i] = *reinterpret_cast<const uint4*>(v_new + src);
+      }
+      tile[i] = ((int64_t)b * a.heads + h) * q4_tile_bytes(D);
+      r[i] = (L - 1) & (kBlock - 1);
     }
-    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-    if (write) {
-      const int64_t src = row * D + g * 64 + j * 8;
-      ku = *reinterpret_cast<const uint4*>(k_new + src);
-      vu = *reinterpret_cast<const uint4*>(v_new + src);
-    }
-    uint32_t kn, vn, word;
-    q4_quantise<T>(ku, vu, lane, &kn, &vn, &word);
-    if (write) {
-      const int64_t tile = ((int64_t)b * a.heads + h) * q4_tile_bytes(D);
-      const int r = (L - 1) % kBlock;
-      uint8_t* kt = static_cast<uint8_t*>(const_cast<void*>(a.k_pool)) + tile;
-      uint8_t* vt = static_cast<uint8_t*>(const_cast<void*>(a.v_pool)) + tile;
-      *reinterpret_cast<uint32_t*>(kt + q4_data_off(g, j, r)) = kn;
-      *reinterpret_cast<uint32_t*>(vt + q4_data_off(g, j, r)) = vn;
-      if ((j & 3) == 0)
-        *reinterpret_cast<uint32_t*>((j == 0 ? kt : vt) + q4_words_off(D) + (g * 16 + r) * 4) = word;
-    }
+    uint32_t kn[U], vn[U], word;
+    q4_quantise<T>(ku, vu, lane, kn, vn, &word);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (write[i]) {
+        uint8_t* kt = static_cast<uint8_t*>(const_cast<void*>(a.k_pool)) + tile[i];
+        uint8_t* vt = static_cast<uint8_t*>(const_cast<void*>(a.v_pool)) + tile[i];
+        *reinterpret_cast<uint32_t*>(kt + q4_data_off(g[i], j, r[i])) = kn[i];
+        *reinterpret_cast<uint32_t*>(vt + q4_data_off(g[i], j, r[i])) = vn[i];
+        if ((j & 3) == 2 * i)
+          *reinterpret_cast<uint32_t*>((j < 4 ? kt : vt) + q4_words_off(D) + (g[i] * 16 + r[i]) * 4) = word;
+      }
   }
 }
 
@@ -300,14 +314,14 @@ __global__ void __launch_bounds__(256)
           ku[u] = *reinterpret_cast<const uint4*>(k_in + row16[u]);
           vu[u] = *reinterpret_cast<const uint4*>(v_in + row16[u]);
         }
+        uint32_t kn[U], vn[U], word;
+        q4_quantise<T>(ku, vu, lane, kn, vn, &word);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          uint32_t kn, vn, word;
-          q4_quantise<T>(ku[u], vu[u], lane, &kn, &vn, &word);
-          *reinterpret_cast<uint32_t*>(k_out + q4_data_off(g[u], j, t[u])) = kn;
-          *reinterpret_cast<uint32_t*>(v_out + q4_data_off(g[u], j, t[u])) = vn;
-          if ((j & 3) == 0)
-            *reinterpret_cast<uint32_t*>((j == 0 ? k_out : v_out) + q4_words_off(D) + (g[u] * 16 + t[u]) * 4) = word;
+          *reinterpret_cast<uint32_t*>(k_out + q4_data_off(g[u], j, t[u])) = kn[u];
+          *reinterpret_cast<uint32_t*>(v_out + q4_data_off(g[u], j, t[u])) = vn[u];
+          if ((j & 3) == 2 * u)
+            *reinterpret_cast<uint32_t*>((j < 4 ? k_out : v_out) + q4_words_off(D) + (g[u] * 16 + t[u]) * 4) = word;
         }
       } else {
         // the largest finite value of T: the last step of a group may pass it
