@@ -1274,8 +1274,10 @@ pa_status pa_convert_blocks(const pa_pool* src, const void* k_src, const void* v
     return fail(PA_ERR_INVALID_ARG, "pa_convert_blocks: pools must be 16-byte aligned");
   DeviceState* dev;
   if ((st = device_state(&dev)) != PA_OK) return st;
-  const int64_t threads = (int64_t)num_pairs * src->heads * 32;  // a warp per (pair, head)
-  const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev->num_sms * 8);
+  // a warp per (pair, head); 16 CTAs an SM, of which 4 run at a time, so that late ones even out
+  // (1024 blocks back to 16 bits: 65 us, with 8 an SM 70)
+  const int64_t threads = (int64_t)num_pairs * src->heads * 32;
+  const int grid = (int)std::min<int64_t>((threads + 255) / 256, (int64_t)dev->num_sms * 16);
   auto kernel = src->dtype == PA_F16       ? q4_convert_kernel<__half, true>
                 : src->dtype == PA_BF16    ? q4_convert_kernel<__nv_bfloat16, true>
                 : src->dtype == PA_Q4_F16  ? q4_convert_kernel<__half, false>

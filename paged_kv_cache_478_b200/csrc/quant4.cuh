@@ -19,9 +19,9 @@
 // fp16 holds every whole number.  The error is at most s / 2, and a few
 // hundredths of s more at the upper end where s was rounded down.  n and z are
 // those of exact quotients (q4_quotient).  Measured (32 heads x 128 fp16):
-// append of 16384 tokens 98 us, 1024 blocks to 4 bits 80 us and back 70 us, for
-// 344 MB each (3.5, 4.3 and 4.9 TB/s): bound by instructions, about 10 a value
-// one way and 8 the other.  A group that holds an infinity or NaN, or whose
+// append of 16384 tokens 88 us, 1024 blocks to 4 bits 73 us and back 65 us, for
+// 344 MB each (3.9, 4.7 and 5.3 TB/s): bound by instructions one way, and by the
+// latency of its loads the other (n - z two at a time, in fp16: no faster).  A group that holds an infinity or NaN, or whose
 // range passes fp32, gets s = NaN and reads back as NaN.
 #pragma once
 
@@ -184,16 +184,22 @@ __global__ void __launch_bounds__(256)
     uint4 ku[U], vu[U];
     int32_t slot[U];
     int h[U], g[U];
+    const int64_t u0 = w * U * 4 + (lane >> 3);
+    int64_t row = u0 >> (groups - 1);  // token * heads + head; groups is 1 or 2
+    int64_t t = q4_div(row, heads);
+    int head = (int)(row - t * heads);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = (w * U + i) * 4 + (lane >> 3);
-      const bool live = u < total;
-      const int64_t row = live ? u >> (groups - 1) : 0;  // token * heads + head; groups is 1 or 2
-      g[i] = live ? (int)(u - row * groups) : 0;
-      const int64_t t = q4_div(row, heads);
-      h[i] = (int)(row - t * heads);
+      const bool live = u0 + 4 * i < total;
+      if (i > 0) {  // four units on
+        row += 4 >> (groups - 1);
+        head += 4 >> (groups - 1);
+        while (head >= heads) head -= heads, ++t;
+      }
+      g[i] = (int)u0 & (groups - 1);
+      h[i] = head;
       slot[i] = live ? slot_mapping[t] : -1;
-      const int64_t src = row * D + g[i] * 64 + j * 8;
+      const int64_t src = live ? row * D + g[i] * 64 + j * 8 : 0;
       ku[i] = *reinterpret_cast<const uint4*>(k_new + src);
       vu[i] = *reinterpret_cast<const uint4*>(v_new + src);
     }
