@@ -17,7 +17,7 @@
 #include "plan.cuh"
 
 // Bound by the latency of one pass over the scores, which mostly are in L2: 9 us
-// beside a decode of 109 us (200 requests x 32 heads, 4-bit), and about 3 us more
+// beside a decode of 98 us (200 requests x 32 heads, 4-bit), and about 3 us more
 // for storing the scores there.
 namespace pa {
 
