@@ -116,6 +116,35 @@ def test_append_of_special_rows(kind):
     assert torch.equal(kd, vd)
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_append_of_quotients_at_and_beside_halves(kind):
+    """Every scale of 8 bits, near zero and far from it: values at k + 1/2 steps, as near as the
+    type holds them, and the type's next numbers above and below."""
+    dim, t = 64, TYPES[kind][0]
+    step, base = np.meshgrid(np.arange(128, 256) / 64.0, [0.0, -7.0, -8.0, 400.0, -1500.0])
+    step, base = step.reshape(-1, 1), base.reshape(-1, 1)
+    half = torch.from_numpy(step * (base + np.arange(15) + 0.5)).to(t)
+    lo, hi = torch.full_like(half, -float("inf")), torch.full_like(half, float("inf"))
+    ends = torch.from_numpy(step * (base + np.array([0.0, 15.0]))).to(t)
+    near = [half, torch.nextafter(half, lo), torch.nextafter(half, hi)]
+    small = torch.from_numpy(step * (base + np.array([2047.0, 2049.0, 1023.0]) / 4096.0)).to(t)
+    x = torch.cat([ends, *near, small], 1)
+    x = torch.cat([x, x[:, :dim - x.shape[1]]], 1)[:, None].contiguous()
+    n = x.shape[0]
+    nb = -(-n // 16)
+    pool = pa.pa_pool_create(nb, 16, 1, dim, TYPES[kind][1])
+    kd = torch.zeros((nb, 1, 9 * dim), dtype=torch.uint8, device="cuda")
+    vd = torch.zeros_like(kd)
+    new = x.cuda()
+    pa.pa_reshape_and_cache(pool, new, -new, torch.arange(n, dtype=torch.int32, device="cuda"), kd, vd)
+    want_k, want_v = np.zeros(kd.shape, dtype=np.uint8), np.zeros(kd.shape, dtype=np.uint8)
+    exact = x.double().numpy()
+    for r in range(n):
+        oc.store_row(want_k, r // 16, 0, r % 16, exact[r, 0])
+        oc.store_row(want_v, r // 16, 0, r % 16, -exact[r, 0])
+    assert np.array_equal(kd.cpu().numpy(), want_k) and np.array_equal(vd.cpu().numpy(), want_v)
+
+
 def test_append_reports_bad_slots_and_writes_nothing_there():
     pool = pa.pa_pool_create(2, 16, 3, 64, pa.PA_Q4_F16)
     k = torch.zeros((2, 3, 576), dtype=torch.uint8, device="cuda")
