@@ -97,23 +97,22 @@ __device__ __forceinline__ uint32_t q4_extent(const uint4& u) {
 // scale, its reciprocal and zero point.
 template <typename T>
 __device__ __forceinline__ uint32_t q4_numbers(const uint4& u, float s, float inv, int z) {
-  if (!(s > 0.f)) return 0u;  // a group of zeros, or s = NaN
+  uint32_t n = 0;
   float x[8];
   Chunk<T>::to_float(u, x);
-  uint32_t n = 0;
-  if (s < 1e-36f) {  // 1 / s or a product may leave the normal numbers: divide
+  if (s >= 1e-36f) {
+    const int off = z - __float_as_int(kRoundMagic);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)  // clamp(round(x / s) + z, 0, 15)
+      n += (uint32_t)__viaddmin_s32_relu(__float_as_int(q4_quotient(x[e], inv)), off, 15) << (4 * e);
+  } else if (s > 0.f) {  // 1 / s or a product may leave the normal numbers: divide
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)) + (float)z, 0.f), 15.f);
       n |= (uint32_t)v << (4 * e);
     }
-    return n;
   }
-  const int off = z - __float_as_int(kRoundMagic);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)  // clamp(round(x / s) + z, 0, 15)
-    n += (uint32_t)__viaddmin_s32_relu(__float_as_int(q4_quotient(x[e], inv)), off, 15) << (4 * e);
-  return n;
+  return n;  // 0 in a group of zeros and where s is NaN
 }
 
 // Quantise two K and two V groups of 64 values (k[u], v[u]), each held by 8
