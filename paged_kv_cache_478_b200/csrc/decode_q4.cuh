@@ -32,10 +32,14 @@
 //     same weights, and even lanes take the first group's scale, odd ones the second's:
 //     one movmatrix makes both groups' operands, and either group's product has
 //     its sums in columns of its own.
-//   P stays within fp16: the softmax reference follows x_t + log2 of the
-//     largest scale of V among the chunk's tokens, and moves (with a rescale of
-//     the accumulators) only when a P could pass 2^15; it is put at 2^10 then,
-//     so that P is a normal number down to 2^-24 of the largest.
+//   The weights' reference m follows the scores alone, w_t = 2^(x_t - m) up to 2^3, so
+//     the softmax sum knows nothing of V.  P stays within fp16 by a factor of its own,
+//     a power of two 2^k for each (head, group): P = w_t s_t,g 2^k.  It is lowered (with
+//     a rescale of the accumulators) only when a P could pass 2^15, so that the chunk's
+//     largest lies at 2^10, and rises again as m does: a P is a normal number down
+//     to 2^-24 of the largest w_t s_t,g so far, whatever the scales of V.  Whether one
+//     could pass 2^15 is told from the chunk's largest weight and largest scale; the
+//     largest product is worked out only then.
 // What bounds it: the unpacking.  Per 16 tokens of a head (2304 bytes of K and V)
 // a warp issued about 310 instructions in fp16, 64 AND, 64 fp16 FMA and 16 matrix ones
 // among them (four or eight heads; with fewer, K's half of that is 16 AND, 16
@@ -122,6 +126,16 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Products of pairs in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // d += a * b for one m16n8k32 tile, a of unsigned bytes, b of signed ones, 32-bit sums.
 __device__ __forceinline__ void mma16832_u8s8(int* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -140,8 +154,13 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
   constexpr int TILE = Cfg::TILE, NSTAGE = Cfg::NSTAGE;
   constexpr int PIECES = D / 32, GROUPS = D / 64;
   constexpr int CB = kQ4ChunkBlocks;
-  // the softmax reference: P stays below 2^(y - ref + 1); it moves beyond kMove, to kPut
-  constexpr float kMove = 14.f, kPut = 10.f;
+  // m follows a score beyond 2^kMove: w s stays below 2^127.2, V's scales being below 2^124.2
+  constexpr float kMove = 3.f;
+  // P's factor 2^k is at most 2^126, lowered where P may pass kPMove, so that the largest lies in [2^10, 2^11):
+  // by biased exponents, that of the largest w s and the factor's add up to kFactorPut
+  constexpr float kPMove = 32768.f;
+  constexpr int kFactorTop = 126 + 127, kFactorPut = 10 + 2 * 127;
+  constexpr int FG = I8 ? 1 : GROUPS;  // groups whose factor a lane keeps (I8: that of its own columns)
 
   extern __shared__ __align__(128) uint8_t q4_smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + Cfg::WARPS * NSTAGE * Cfg::STAGE_BYTES);
@@ -210,9 +229,14 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
 
     // of query heads 2 j + e (I8: heads e, the same in the quad's lanes); l_run is over this lane's tokens
-    float ref[NH], l_run[NH];
+    float m[NH], l_run[NH];
+    float f[FG][NH];
 #pragma unroll
-    for (int e = 0; e < NH; ++e) ref[e] = -INFINITY, l_run[e] = 0.f;
+    for (int e = 0; e < NH; ++e) {
+      m[e] = -INFINITY, l_run[e] = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < FG; ++gr) f[gr][e] = __uint_as_float((uint32_t)kFactorTop << 23);
+    }
     float o[PIECES][2][4];
 #pragma unroll
     for (int c = 0; c < PIECES; ++c)
@@ -442,16 +466,33 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           }
         }
 
-        // ---- softmax: the chunk's maxima and its largest V scale
-        float mx[NH];
+        // ---- softmax: the chunk's maxima, and the weights in the scores' place
+        float mx[NH], down[NH];  // down: what m moves the accumulators by, in log2
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
           mx[e] = -INFINITY;
 #pragma unroll
           for (int b = 0; b < CB; ++b) mx[e] = fmaxf(mx[e], fmaxf(x[b][0][e], x[b][1][e]));
 #pragma unroll
-          for (int m = 4; m < 32; m <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFullMask, mx[e], m));
+          for (int k = 4; k < 32; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFullMask, mx[e], k));
+          if constexpr (!I8) mx[e] *= kq[e];
+          down[e] = 0.f;
+          if (mx[e] > m[e] + kMove) {
+            down[e] = m[e] - mx[e];  // -infinity on the first move
+            m[e] = mx[e];
+            l_run[e] *= ex2(down[e]);
+          }
+          const float mb = m[e] == -INFINITY ? 0.f : -m[e];
+#pragma unroll
+          for (int b = 0; b < CB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              x[b][nt][e] = ex2(I8 ? x[b][nt][e] + mb : fmaf(x[b][nt][e], kq[e], mb));
+              l_run[e] += x[b][nt][e];
+            }
         }
+
+        // ---- P's factors
         uint32_t big = 0u;
         constexpr int WPB = 4 * GROUPS;  // 16-byte loads that hold a block's words
         if (lane < CB * WPB) {
@@ -462,47 +503,53 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int e = 0; e < 4; ++e)
             if (ws[e] < 0x7f800000u) big = max(big, ws[e]);  // NaN scales do not count
         }
-        big = __reduce_max_sync(kFullMask, big);
-        // not below 2^-90 (no scale at all: V is zero): the weights reach 2^(90 + kMove), of which 2^23 add up in fp32
-        const float ev = (float)max((int)(big >> 23) - 127, -90);
-        float y[NH];
+        big = __reduce_max_sync(kFullMask, big);  // as a float, the largest scale and a little more
         bool move = false;
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
-          y[e] = I8 ? mx[e] + ev : fmaf(mx[e], kq[e], ev);
-          move |= y[e] > ref[e] + kMove;
+          const float bound = __uint_as_float(big) * ex2(mx[e] - m[e]);
+          move |= down[e] < 0.f;
+#pragma unroll
+          for (int gr = 0; gr < FG; ++gr) move |= bound * f[gr][e] > kPMove;
         }
         if (__any_sync(kFullMask, move)) {
-          float alpha[2] = {1.f, 1.f};
 #pragma unroll
-          for (int e = 0; e < NH; ++e)
-            if (y[e] > ref[e] + kMove) {
-              alpha[e] = ex2(ref[e] - (y[e] - kPut));  // 0 on the first move
-              ref[e] = y[e] - kPut;
-              l_run[e] *= alpha[e];
+          for (int gr = 0; gr < FG; ++gr) {
+            float top[NH], alpha[2] = {1.f, 1.f};  // top: the group's largest w s
+#pragma unroll
+            for (int e = 0; e < NH; ++e) top[e] = 0.f;
+#pragma unroll
+            for (int b = 0; b < CB; ++b)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(
+                    vt + b * TILE + q4_words_off(D) + (I8 ? (GROUPS == 2 ? j & 1 : 0) : gr) * 64 + nt * 32 + r * 4));
+#pragma unroll
+                for (int e = 0; e < NH; ++e) top[e] = fmaxf(top[e], x[b][nt][e] * sc);  // NaN does not count
+              }
+#pragma unroll
+            for (int e = 0; e < NH; ++e) {
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(kFullMask, top[e], k));
+              const int was = (int)(__float_as_uint(f[gr][e]) >> 23), ex = (int)(__float_as_uint(top[e]) >> 23);
+              int fe = was;
+              if (down[e] < 0.f) fe = min(kFactorTop, fe + (int)fminf(-down[e], 512.f));  // rises as m does
+              if (top[e] * __uint_as_float((uint32_t)fe << 23) > kPMove) fe = kFactorPut - ex;
+              alpha[e] = ex2(down[e] + (float)(fe - was));  // 0 on the first move
+              f[gr][e] = __uint_as_float((uint32_t)fe << 23);
             }
 #pragma unroll
-          for (int c = 0; c < PIECES; ++c)
+            for (int c = gr * (PIECES / FG); c < (gr + 1) * (PIECES / FG); ++c)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[c][m][e] *= alpha[NH == 2 ? e & 1 : 0];
+                for (int e = 0; e < 4; ++e) o[c][h][e] *= alpha[NH == 2 ? e & 1 : 0];
+          }
         }
-        float mb[NH];
-#pragma unroll
-        for (int e = 0; e < NH; ++e) mb[e] = ref[e] == -INFINITY ? 0.f : -ref[e];
 
         // ---- values
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
-          float w[2][NH];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < NH; ++e) {
-              w[nt][e] = ex2(I8 ? x[b][nt][e] + mb[e] : fmaf(x[b][nt][e], kq[e], mb[e]));
-              l_run[e] += w[nt][e];
-            }
           const uint32_t tile = smem_addr(vt + b * TILE);
           const uint8_t* words = vt + b * TILE + q4_words_off(D);
           uint32_t pc[2];  // I8: the quad's lanes take the groups' P in turn, each in columns of its own
@@ -511,7 +558,9 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             for (int nt = 0; nt < 2; ++nt) {
               const float sc = q4_scale(
                   *reinterpret_cast<const uint32_t*>(words + (GROUPS == 2 ? (j & 1) * 64 : 0) + nt * 32 + r * 4));
-              pc[nt] = movmatrix(pack_half(w[nt][0] * sc, NH == 2 ? w[nt][NH - 1] * sc : 0.f));
+              const float2 p = mul2(mul2(make_float2(x[b][nt][0], x[b][nt][NH - 1]), make_float2(sc, sc)),
+                                    make_float2(f[0][0], f[0][NH - 1]));
+              pc[nt] = movmatrix(pack_half(p.x, NH == 2 ? p.y : 0.f));
             }
           }
 #pragma unroll
@@ -524,7 +573,9 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
                 pb[nt] = pc[nt];
               } else {
                 const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
-                pb[nt] = movmatrix(pack_half(w[nt][0] * sc, w[nt][NH - 1] * sc));
+                const float2 p = mul2(mul2(make_float2(x[b][nt][0], x[b][nt][NH - 1]), make_float2(sc, sc)),
+                                      make_float2(f[gr % FG][0], f[gr % FG][NH - 1]));
+                pb[nt] = movmatrix(pack_half(p.x, p.y));
               }
               const uint2 two = *reinterpret_cast<const uint2*>(words + gr * 64 + nt * 32 + j * 8);
               nz[nt] = __hmul2(as_half2(__byte_perm(two.x, two.y, 0x5410)), as_half2(kMinus2m10));
@@ -563,7 +614,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 #pragma unroll
       for (int e = 0; e < NH; ++e)
 #pragma unroll
-        for (int m = 4; m < 32; m <<= 1) l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], m);
+        for (int k = 4; k < 32; k <<= 1) l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], k);
       if (wph > 1 && part > 0) {  // for the first warp of the head (this warp's stages are drained)
         float* xs = reinterpret_cast<float*>(my_stages);
 #pragma unroll
@@ -574,8 +625,11 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             for (int e = 0; e < 4; ++e) xs[((c * 2 + m) * 4 + e) * 32 + lane] = o[c][m][e];
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
-          xs[(PIECES * 8 + 2 * e) * 32 + lane] = ref[e];
+          xs[(PIECES * 8 + 2 * e) * 32 + lane] = m[e];
           xs[(PIECES * 8 + 2 * e + 1) * 32 + lane] = l_run[e];
+#pragma unroll
+          for (int gr = 0; gr < FG; ++gr)
+            xs[(PIECES * 8 + 2 * NH + gr * NH + e) * 32 + lane] = f[gr][e];
         }
         fence_proxy_async_shared();  // before the ring's next bulk copies into the same bytes
       }
@@ -584,40 +638,60 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     if (mine && part == 0 && (wph > 1 ? !s_abort : ok)) {
       for (int other = 1; other < wph; ++other) {  // fold in the other warps' states
         const float* xs = reinterpret_cast<const float*>(my_stages + other * NSTAGE * Cfg::STAGE_BYTES);
-        float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+        float sa[FG][2] = {}, sb[FG][2] = {};  // rescales of the accumulators
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
-          const float rb = xs[(PIECES * 8 + 2 * e) * 32 + lane], lb = xs[(PIECES * 8 + 2 * e + 1) * 32 + lane];
-          const float M = fmaxf(ref[e], rb);
-          sa[e] = ref[e] == -INFINITY ? 0.f : exp2f(ref[e] - M);
-          sb[e] = rb == -INFINITY ? 0.f : exp2f(rb - M);
-          l_run[e] = l_run[e] * sa[e] + lb * sb[e];
-          ref[e] = M;
+          const float mb = xs[(PIECES * 8 + 2 * e) * 32 + lane], lb = xs[(PIECES * 8 + 2 * e + 1) * 32 + lane];
+          const float M = fmaxf(m[e], mb);
+          l_run[e] = (m[e] == -INFINITY ? 0.f : l_run[e] * exp2f(m[e] - M)) + (mb == -INFINITY ? 0.f : lb * exp2f(mb - M));
+#pragma unroll
+          for (int gr = 0; gr < FG; ++gr) {
+            // either factor, risen as M lies above its reference; the smaller one serves both
+            const float other = xs[(PIECES * 8 + 2 * NH + gr * NH + e) * 32 + lane];
+            const int fa = (int)(__float_as_uint(f[gr][e]) >> 23), fb = (int)(__float_as_uint(other) >> 23);
+            const int both = min(kFactorTop, min(fa + (int)fminf(M - m[e], 512.f), fb + (int)fminf(M - mb, 512.f)));
+            sa[gr][e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - M + (float)(both - fa));
+            sb[gr][e] = mb == -INFINITY ? 0.f : exp2f(mb - M + (float)(both - fb));
+            f[gr][e] = __uint_as_float((uint32_t)both << 23);
+          }
+          m[e] = M;
         }
 #pragma unroll
         for (int c = 0; c < PIECES; ++c)
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[c][m][e] = o[c][m][e] * sa[NH == 2 ? e & 1 : 0] +
-                           xs[((c * 2 + m) * 4 + e) * 32 + lane] * sb[NH == 2 ? e & 1 : 0];
+            for (int e = 0; e < 4; ++e) {
+              const int gr = c / (PIECES / FG), head = NH == 2 ? e & 1 : 0;
+              o[c][h][e] = o[c][h][e] * sa[gr][head] + xs[((c * 2 + h) * 4 + e) * 32 + lane] * sb[gr][head];
+            }
       }
       if (wph > 1) fence_proxy_async_shared();  // the other warps' rings are refilled after the loop's barrier
+      // The accumulators hold 2^(k - 10) of their sums.  Partial results are the sums over (1 to 2) 2^12 of l, with
+      // m raised by as much: whatever the values, thousands of them add up in fp32, and small ones stay.
+      float inv[NH];
+      float2 ml[NH];
+#pragma unroll
+      for (int e = 0; e < NH; ++e) {
+        const int up = (int)(__float_as_uint(l_run[e]) >> 23) - 127 + 12;
+        const float by = __uint_as_float((uint32_t)(127 - up) << 23);
+        inv[e] = split ? 1024.f * by : m[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
+        ml[e] = make_float2(m[e] + (float)up, l_run[e] * by);
+      }
+      // 2^-k
+      auto back = [&](int gr, int e) { return __uint_as_float((254u << 23) - __float_as_uint(f[gr % FG][e])); };
       if constexpr (I8) {
         // the lanes of a quad hold the same heads; with two groups, even lanes the first one's dimensions, odd
         // ones the second's: each writes a piece
         const int piece = GROUPS == 2 ? 2 * (j & 1) + (j >> 1) : j;
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
-          // the accumulators hold 2^-10 of their sums
-          const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
           float v[4];
 #pragma unroll
           for (int c = 0; c < PIECES; ++c)
             if (c == piece) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = o[c][k >> 1][2 * (k & 1) + e] * inv;
+              for (int k = 0; k < 4; ++k) v[k] = o[c][k >> 1][2 * (k & 1) + e] * inv[e] * back(0, e);
             }
           if (piece < PIECES) {
             if (!split)
@@ -628,8 +702,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
                   make_float4(v[0], v[1], v[2], v[3]);
           }
           if (lane == 0) {
-            if (split) a.part_ml[(sh0 + e) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
-            else if (MASS) a.lse[sh0 + e] = ref[e] + log2f(l_run[e]);
+            if (split) a.part_ml[(sh0 + e) * a.max_parts + p] = ml[e];
+            else if (MASS) a.lse[sh0 + e] = m[e] + log2f(l_run[e]);
           }
         }
       } else {
@@ -638,11 +712,11 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         for (int e = 0; e < NH; ++e) {
           const int h = 2 * j + e;
           if (h >= G) continue;
-          // the accumulators hold 2^-10 of their sums
-          const float inv = split ? 1024.f : ref[e] != -INFINITY ? 1024.f / l_run[e] : 0.f;
 #pragma unroll
           for (int c = 0; c < PIECES; ++c) {
-            const float v[4] = {o[c][0][e] * inv, o[c][0][2 + e] * inv, o[c][1][e] * inv, o[c][1][2 + e] * inv};
+            const float lift = back(c / 2, e);
+            const float v[4] = {o[c][0][e] * inv[e] * lift, o[c][0][2 + e] * inv[e] * lift, o[c][1][e] * inv[e] * lift,
+                                o[c][1][2 + e] * inv[e] * lift};
             if (!split) {
               *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
                   make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
@@ -652,8 +726,8 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
             }
           }
           if (r == 0) {
-            if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = make_float2(ref[e], l_run[e]);
-            else if (MASS) a.lse[sh0 + h] = ref[e] + log2f(l_run[e]);
+            if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = ml[e];
+            else if (MASS) a.lse[sh0 + h] = m[e] + log2f(l_run[e]);
           }
         }
       }

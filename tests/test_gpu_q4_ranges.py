@@ -1,0 +1,158 @@
+"""Decode over 4-bit pools whose keys and values differ in size by many powers of two, on
+the GPU against the fp64 oracle: the softmax sum must not depend on the values, nor small
+values of the attended tokens on large ones of tokens that are not attended.
+
+Tolerance, from the arithmetic (L tokens, D dimensions, w the normalised weights, s a group's
+scale, n - z a held value; every bound is for one dimension of one head):
+  * the output's own rounding, eps / 2 of it (and half a subnormal step);
+  * scores: fp32 sums, off by at most D 2^-24 scale sum |q| s (n + |z|) + 2^-22 =: e, numerator
+    and denominator: 2 e sum w |v|;
+  * P = w s 2^k rounded to fp16: 2^-11 of it, and where it is subnormal 2^-25.  2^k puts the
+    largest w s so far at 2^10 or above (2^3 at least where k meets its limit of 126: scales down
+    to 2^-123): a subnormal is off by 2^-28 of the largest, times |n - z|;
+  * the sum of the numerator: L 2^-23 sum w |v|;
+  * weights below 2^-126 of the largest are zero: L 2^-125 max |v|;
+  * partial results: the running maximum plus a whole number, below 2^7, is off by 2^-18, a
+    weight of a partition by as much: 2^-17 sum w |v|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_478_b200 as pa
+from oracle import compress as oc
+from tests.test_gpu_q4 import TYPES, as_type, check, cuda, decode_case, run_decode
+
+pytestmark = pytest.mark.gpu
+
+ROUNDED = 2.0 ** -11  # of a weight times its scale
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    if torch.cuda.is_available():
+        pa.pa_device_errors()
+    yield
+
+
+def sized(k_size, v_size):
+    """Rows N(0, 1) times a size per token (and dimension): K first, then V, as decode_case draws them."""
+    sizes = [np.asarray(k_size, dtype=np.float64), np.asarray(v_size, dtype=np.float64)]
+
+    def spread(rng, n, heads, dim):
+        size = sizes.pop(0)
+        size = np.broadcast_to(size.reshape(-1, 1, size.shape[1] if size.ndim == 2 else 1), (n, 1, size.shape[1] if size.ndim == 2 else 1))
+        return rng.standard_normal((n, heads, dim)) * size
+
+    return spread
+
+
+def expected(c):
+    """Output, its tolerance and the weights of a decode_case."""
+    dim, (ns, ss, zs) = c["dim"], oc.parts(c["vp"], c["dim"])
+    kn, ks, kz = oc.parts(c["kp"], dim)
+    kmag = np.repeat(ks, 64, -1) * (kn + np.abs(np.repeat(kz, 64, -1)))
+    held = np.abs(ns - np.repeat(zs, 64, -1))
+    v = oc.values(c["vp"], dim)
+    out, weights, bound = oc.attend(c["qx"], oc.values(c["kp"], dim), v, c["lens"], c["tables"], c["scale"])
+    fi = torch.finfo(TYPES[c["kind"]][0])
+    tol, rel = np.zeros_like(out), [np.zeros(out.shape[1]) for _ in c["lens"]]
+    for i, L in enumerate(c["lens"]):
+        b, r = c["tables"][i, np.arange(L) // 16], np.arange(L) % 16
+        for h in range(out.shape[1] if L else 0):
+            hk, w = h // c["group"], weights[i][h]
+            e = dim * 2.0 ** -24 * abs(c["scale"]) * (kmag[b, hk, r] @ np.abs(c["qx"][i, h])).max() + 2.0 ** -22
+            largest = np.repeat((w[:, None] * ss[b, hk, r]).max(0), 64) * np.repeat(held[b, hk, r].reshape(L, -1, 64).max((0, 2)), 64)
+            tol[i, h] = (fi.eps / 2 * 1.01 * np.abs(out[i, h]) + fi.smallest_normal * fi.eps / 2
+                         + (ROUNDED * 1.01 + 2.02 * e + L * 2.0 ** -23 + 2.0 ** -17) * bound[i, h]
+                         + L * 2.0 ** -28 * largest + L * 2.0 ** -125 * np.abs(v[b, hk, r]).max(0))
+            rel[i][h] = 2 * e + 2.0 ** -17
+    return out, tol, weights, rel
+
+
+def check_decode_and_mass(c, partitions=(0, 16, 64, 208)):
+    want, tol, weights, rel = expected(c)
+    S, HQ = want.shape[:2]
+    pool = pa.pa_pool_set_query_heads(pa.pa_pool_create(c["kp"].shape[0], 16, c["heads"], c["dim"], TYPES[c["kind"]][1]), HQ)
+    k, v, bt, cl = (cuda(c[n]) for n in ("kp", "vp", "tables", "lens"))
+    for partition in partitions:
+        got = run_decode(c, partition)
+        check(got, want, tol)
+        ws = torch.empty(pa.pa_decode_mass_workspace_bytes(pool, S, bt.shape[1], 0, partition), dtype=torch.uint8, device="cuda")
+        out, mass = torch.empty_like(c["q"]), torch.zeros((S, bt.shape[1] * 16), device="cuda")
+        pa.pa_decode_attention_mass(pool, c["q"], k, v, bt, cl, c["scale"], out, None, mass, ws, partition_size=partition)
+        assert pa.pa_device_errors() == 0 and torch.equal(out, got)
+        for i, L in enumerate(c["lens"]):
+            # the weights, which know nothing of V: a factor of 1 + rel each, (HQ + 2) 2^-24 for their sum
+            off = np.abs(mass[i, :L].double().cpu().numpy() - weights[i].sum(0))
+            assert (off <= (rel[i][:, None] * weights[i]).sum(0) + (HQ + 2) * 2.0 ** -24 * weights[i].sum(0) + HQ * 2.0 ** -125).all()
+
+
+# ---- values of every size, comparable scores -------------------------------------------------
+
+SIZES = {"zeros_then_1e14": lambda t: np.where(t < 64, 0, 1e14), "1e14_then_zeros": lambda t: np.where(t < 64, 1e14, 0),
+         "tiny_then_huge": lambda t: np.where(t < 64, 1e-30, 1e30), "huge_then_tiny": lambda t: np.where(t < 64, 1e30, 1e-30),
+         "rising": lambda t: 10.0 ** (t / 5 - 36), "falling": lambda t: 10.0 ** (36 - t / 5), "mixed": lambda t: 10.0 ** (t * 7919 % 73 - 36),
+         "zeros_amid_huge": lambda t: np.where(t % 3, 0, 1e37)}
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("heads,group,dim", [(1, 1, 64), (6, 1, 128), (2, 2, 128), (1, 4, 64), (4, 4, 128), (2, 8, 128)])
+def test_values_of_very_different_sizes(sizes, heads, group, dim):
+    lengths = [360, 129, 1] if heads * group <= 8 else [300]
+    t = np.concatenate([np.arange(n) for n in lengths])
+    c = decode_case(heads + group + dim, lengths, heads, group, dim, "bf16", sized(np.full(len(t), 0.5), SIZES[sizes](t)))
+    check_decode_and_mass(c)
+
+
+# ---- large values that are not attended --------------------------------------------------------
+
+def shunned(kind, group, dim, at, big, small, away, heads=1, turned=False):
+    """`small` values everywhere but at the tokens `at`, whose values are `big` and whose scores lie `away` (natural
+    units) below the others.  turned: the group's last query head attends to those instead."""
+    L = 330
+    c = decode_case(7 * group + dim, [L], heads, group, dim, kind, sized(np.full(L, 0.02), np.where(np.isin(np.arange(L), at), big, small)))
+    base = np.random.default_rng(5).standard_normal(dim)
+    qx = base + 0.05 * np.random.default_rng(6).standard_normal((1, heads * group, dim))
+    if turned:
+        qx[:, group - 1::group] *= -1
+    c["q"], c["qx"] = as_type(qx, kind)
+    row = -away / (c["scale"] * (base @ base)) * base
+    for t in at:
+        for h in range(heads):
+            oc.store_row(c["kp"], c["tables"][0, t // 16], h, t % 16, as_type(row, kind)[1])
+    return c
+
+
+@pytest.mark.parametrize("at", [[0], [40], [329], [3, 70, 200]])
+@pytest.mark.parametrize("kind,big,small,away", [("f16", 1e4, 1e-4, 45.0), ("bf16", 1e20, 1.0, 70.0), ("bf16", 1e30, 1e-3, 80.0)])
+@pytest.mark.parametrize("group,dim", [(1, 64), (1, 128), (2, 128), (4, 128), (8, 64)])
+def test_large_values_that_are_not_attended(kind, big, small, away, group, dim, at):
+    check_decode_and_mass(shunned(kind, group, dim, at, big, small, away), (0, 64))
+
+
+@pytest.mark.parametrize("group", [2, 4, 8])
+def test_heads_that_attend_to_values_of_different_sizes(group):
+    check_decode_and_mass(shunned("bf16", group, 128, [10, 100], 1e20, 1.0, 70.0, heads=2, turned=True), (0, 64))
+
+
+@pytest.mark.parametrize("kind,ratio", [("f16", 2.0 ** 24), ("bf16", 2.0 ** 60), ("bf16", 2.0 ** -60)])
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+def test_groups_of_different_sizes(kind, ratio, group):
+    """A row's two groups of 64 dimensions, one far larger than the other."""
+    size = np.where(np.arange(128) < 64, 2.0 ** -12, 2.0 ** -12 * ratio)[None].repeat(200, 0)
+    check_decode_and_mass(decode_case(group, [200], 2, group, 128, kind, sized(np.full(200, 1.0), size)), (0, 64))
+
+
+# ---- the ends of the type's range -----------------------------------------------------------------
+
+@pytest.mark.parametrize("size", [1e-37, 3e-36, 1e-33, 8e37])
+@pytest.mark.parametrize("group", [1, 2, 4])
+def test_values_at_the_ends_of_the_range(size, group):
+    """bf16 values near the smallest normal numbers, and so near the largest that their sum is not finite."""
+    def spread(rng, n, heads, dim):
+        return size * np.sign(rng.standard_normal((1, heads, dim))) * (1 + rng.random((n, heads, dim)))
+
+    rows = iter([lambda rng, n, h, d: rng.standard_normal((n, h, d)), spread])
+    c = decode_case(group, [300, 40], 2, group, 64, "bf16", lambda *a: next(rows)(*a))
+    check_decode_and_mass(c)
