@@ -119,6 +119,16 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   return r;
 }
 
+// 2^p of a whole number from -126 to 127.
+__device__ __forceinline__ float pow2(int p) { return __uint_as_float((uint32_t)(p + 127) << 23); }
+
+// scale * 2^p as two factors, for before and after the product with K's scale, which neither then takes out of
+// fp32 where the score itself is in it.  The second is 1 but for queries of extreme sizes.
+__device__ __forceinline__ float2 split_factor(float scale, int p) {
+  return p > 0 ? make_float2(1.f, scale * pow2(p))
+               : p < -64 ? make_float2(pow2(-64), scale * pow2(p + 64)) : make_float2(scale * pow2(p), 1.f);
+}
+
 // 2^x; results below the normal numbers become zero.
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
       // Q fragments, column r, dimensions 32 c + 8 j .. + 7: head r (I8: digit r / 2 of head r % 2); columns
       // past G are zero
       uint32_t qb[PIECES][I8 ? 2 : 4];
-      float kq[NH];          // scores to log2 units (I8: of this lane's digit)
+      float2 kq[NH];         // scores to log2 units, in two factors (I8: of this lane's digit)
       float qs[GROUPS][NH];  // I8: sum of a group's queries in this lane's digit
       {
         const int q_head = I8 ? (r & 1) : r;
@@ -295,12 +305,12 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           // as whole numbers, the row's largest in [2^21, 2^22), of three signed base-256 digits; column r
           // is digit r / 2, the leading one first, of head r % 2
           const int term = r >> 1;
-          const int qe = ex == 255 ? 0 : min(21 + 127 - ex, 126);
-          const float f = __uint_as_float((uint32_t)(qe + 127) << 23);
+          const int qe = ex == 255 ? 0 : 21 + 127 - ex;
+          const float fa = pow2(qe >> 1), fb = pow2(qe - (qe >> 1));  // 2^qe
           float probe = 0.f;  // NaN once a query is NaN or infinite
           auto digit = [&](float x, int* sum) {
             probe = fmaf(x, 0.f, probe);
-            const int v = __float2int_rn(x * f);
+            const int v = __float2int_rn(x * fa * fb);
             const int d0 = (int)(int8_t)v, v1 = (v - d0) >> 8;
             const int d1 = (int)(int8_t)v1, d2 = (v1 - d1) >> 8;
             const int d = term == 0 ? d2 : term == 1 ? d1 : term == 2 ? d0 : 0;
@@ -324,26 +334,29 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           }
           probe += __shfl_xor_sync(kFullMask, probe, 1);
           probe += __shfl_xor_sync(kFullMask, probe, 2);
-          const float mine_kq = __uint_as_float((uint32_t)(127 - qe) << 23) + probe;
-          const float kj = a.scale_log2 * __uint_as_float((uint32_t)(127 + 16 - 8 * j) << 23);  // the digit's weight
 #pragma unroll
-          for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 4 * e) * kj;
+          for (int e = 0; e < NH; ++e)  // 2^(16 - 8 j): the digit's weight
+            kq[e] = split_factor(a.scale_log2 + __shfl_sync(kFullMask, probe, 4 * e),
+                                 16 - 8 * j - __shfl_sync(kFullMask, qe, 4 * e));
         } else {
-          // scaled by 2^qe so that the row's largest value lies in [2^14, 2^15); a negative scale turns Q
-          const int qe = ex == 255 ? 0 : min(14 + 127 - ex, 100);
-          const float f = copysignf(__uint_as_float((uint32_t)(qe + 127) << 23), a.scale_log2);
-          // 2^(10 - qe); never zero, so that a masked score stays -infinity when the scale is 0
-          const float mine_kq = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + 10 - qe) << 23),
-                                      1.17549435e-38f);
+          // scaled by 2^qe so that the row's largest value lies in [2^14, 2^15)
+          const int qe = ex == 255 ? 0 : 14 + 127 - ex;
+          const float fa = pow2(qe >> 1), fb = pow2(qe - (qe >> 1));
 #pragma unroll
-          for (int e = 0; e < NH; ++e) kq[e] = __shfl_sync(kFullMask, mine_kq, 8 * j + 4 * e);
+          for (int e = 0; e < NH; ++e)
+            kq[e] = split_factor(a.scale_log2, 10 - __shfl_sync(kFullMask, qe, 8 * j + 4 * e));
 #pragma unroll
           for (int c = 0; c < PIECES; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // pairs as the nibbles lie in a register: (0, 4), (1, 5), ...
-              qb[c][e] = pack_half(qf[c][e] * f, qf[c][e + 4] * f);
+              qb[c][e] = pack_half(qf[c][e] * fa * fb, qf[c][e + 4] * fa * fb);
         }
       }
+
+      bool second = false;  // a second factor is not 1
+#pragma unroll
+      for (int e = 0; e < NH; ++e) second |= kq[e].y != 1.f;
+      second = __any_sync(kFullMask, second);
 
       int i = 0;
       for (; i < c_n; ++i) {
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           __syncwarp();
         }
 
-        // ---- scores of the chunk, raw or (I8) in log2 units: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e (e)
+        // ---- scores of the chunk in log2 units: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e (e)
         float x[CB][2][NH];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
@@ -393,22 +406,24 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
                 const uint32_t am[4] = {w0 & kNibbles, w1 & kNibbles, (w0 >> 4) & kNibbles, (w1 >> 4) & kNibbles};
                 mma16832_u8s8(c, am, qb[pc][0], qb[pc][1]);
               }
+              uint32_t word[2];
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                const uint32_t word = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
-                const float sc = q4_scale(word), z = q4_zero(word);
+              for (int nt = 0; nt < 2; ++nt) word[nt] = *reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32);
 #pragma unroll
-                for (int e = 0; e < NH; ++e) {
-                  const float d = fmaf(-z, qs[gr][e], (float)c[2 * nt + e]);
-                  x[b][nt][e] = gr == 0 ? sc * d : fmaf(sc, d, x[b][nt][e]);
-                }
+              for (int e = 0; e < NH; ++e) {
+                const float2 d = mul2(make_float2(fmaf(-q4_zero(word[0]), qs[gr][e], (float)c[e]),
+                                                  fmaf(-q4_zero(word[1]), qs[gr][e], (float)c[2 + e])),
+                                      make_float2(kq[e].x, kq[e].x));
+                x[b][0][e] = gr == 0 ? q4_scale(word[0]) * d.x : fmaf(q4_scale(word[0]), d.x, x[b][0][e]);
+                x[b][1][e] = gr == 0 ? q4_scale(word[1]) * d.y : fmaf(q4_scale(word[1]), d.y, x[b][1][e]);
               }
             }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int e = 0; e < NH; ++e) {  // the digits, over the quad's lanes
-                float v = x[b][nt][e] * kq[e];
+                float v = x[b][nt][e];
+                if (second) v *= kq[e].y;
                 v += __shfl_xor_sync(kFullMask, v, 1);
                 v += __shfl_xor_sync(kFullMask, v, 2);
                 x[b][nt][e] = v;
@@ -433,12 +448,18 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
                 mma16816<__half>(c, a1, qb[pc][2], qb[pc][3]);
               }
 #pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                const float sc = q4_scale(word[nt]);
+                const float2 d = mul2(make_float2(c[2 * nt], c[2 * nt + 1]), make_float2(kq[0].x, kq[NH - 1].x));
+                x[b][nt][0] = gr == 0 ? sc * d.x : fmaf(sc, d.x, x[b][nt][0]);
+                x[b][nt][NH - 1] = gr == 0 ? sc * d.y : fmaf(sc, d.y, x[b][nt][NH - 1]);
+              }
+            }
+            if (second) {
+#pragma unroll
               for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < NH; ++e) {
-                  const float sc = q4_scale(word[nt]);
-                  x[b][nt][e] = gr == 0 ? sc * c[2 * nt + e] : fmaf(sc, c[2 * nt + e], x[b][nt][e]);
-                }
+                for (int e = 0; e < NH; ++e) x[b][nt][e] *= kq[e].y;
             }
           }
         }
@@ -462,7 +483,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt)  // I8: the quad's lanes hold the same, and store a block each
                 if ((!I8 || (b & 3) == j) && b * 16 + nt * 8 + r < valid)
-                  dst[b * 16 + nt * 8] = I8 ? x[b][nt][e] : x[b][nt][e] * kq[e];
+                  dst[b * 16 + nt * 8] = x[b][nt][e];
           }
         }
 
@@ -475,7 +496,6 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int b = 0; b < CB; ++b) mx[e] = fmaxf(mx[e], fmaxf(x[b][0][e], x[b][1][e]));
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFullMask, mx[e], k));
-          if constexpr (!I8) mx[e] *= kq[e];
           down[e] = 0.f;
           if (mx[e] > m[e] + kMove) {
             down[e] = m[e] - mx[e];  // -infinity on the first move
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           for (int b = 0; b < CB; ++b)
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              x[b][nt][e] = ex2(I8 ? x[b][nt][e] + mb : fmaf(x[b][nt][e], kq[e], mb));
+              x[b][nt][e] = ex2(x[b][nt][e] + mb);
               l_run[e] += x[b][nt][e];
             }
         }

@@ -156,3 +156,22 @@ def test_values_at_the_ends_of_the_range(size, group):
     rows = iter([lambda rng, n, h, d: rng.standard_normal((n, h, d)), spread])
     c = decode_case(group, [300, 40], 2, group, 64, "bf16", lambda *a: next(rows)(*a))
     check_decode_and_mass(c)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("group,dim", [(1, 64), (2, 128), (8, 128)])
+def test_one_token_returns_its_value(kind, group, dim):
+    """A single weight is 1: the output is the held value, rounded once to the type."""
+    c = decode_case(group, [1, 1, 1], 2, group, dim, kind, sized(np.full(3, 30.0), [1.0, 100.0, 1e-3]))
+    v = oc.values(c["vp"], dim)[c["tables"][:, 0], :, 0]
+    want = torch.from_numpy(v).to(TYPES[kind][0]).repeat_interleave(group, 1)
+    assert torch.equal(run_decode(c).cpu(), want)
+
+
+@pytest.mark.parametrize("k_size", [3e37, 1e34, 1e30, 1e-30, 3e-36])
+@pytest.mark.parametrize("heads,group,dim", [(1, 1, 64), (2, 1, 128), (3, 2, 64), (2, 4, 128), (1, 8, 128)])
+def test_keys_at_the_ends_of_the_range(k_size, heads, group, dim):
+    """Keys near the ends of bf16's range with queries near the other one: ordinary scores."""
+    c = decode_case(group * dim, [200, 17], heads, group, dim, "bf16", sized(np.full(217, k_size), np.full(217, 1.0)))
+    c["q"], c["qx"] = as_type(c["qx"] / k_size, "bf16")
+    check_decode_and_mass(c, (0, 64))
