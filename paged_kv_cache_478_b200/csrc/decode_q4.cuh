@@ -23,15 +23,17 @@
 //     lanes, which hold a digit each, add their shares in fp32.
 //     Four or eight heads need the columns: fp16, Q scaled by a power of two into
 //     its range, fp32 sums.  A lane gets the scores of tokens lane / 4 and lane / 4 + 8
-//     of each block and of heads 2 (lane % 4) and the next.
+//     of each block and of heads 2 (lane % 4) and the next (of four heads, lane % 2).
 //     In both, one word a token and group gives its zero point and its scale.
 //   values:  o_d = sum_t P_t,g (n_t,d - z_t,g),  P_t,g = w_t s_t,g.
-//     V^T is the A operand in fp16; P, rounded to fp16 once (2^-11) and transposed
-//     8 x 8 by movmatrix, the B operand, so its accumulators belong to the same two
-//     heads as the lane's softmax state.  With one or two heads the quad's lanes hold the
-//     same weights, and even lanes take the first group's scale, odd ones the second's:
-//     one movmatrix makes both groups' operands, and either group's product has
-//     its sums in columns of its own.
+//     V^T is the A operand in fp16, exact; P, transposed 8 x 8 by movmatrix, the B
+//     operand, as two fp16 numbers: its value and what that rounding left (2^-21 of P
+//     together; the first alone, 2^-11, showed in outputs whose terms cancel).  Its
+//     columns are the heads, in the lanes that hold their scores, times the groups
+//     (up to four heads), times the two parts where room is left (one or two heads,
+//     or four at head_dim 64); else the second part takes products of its own.  The
+//     quad's lanes hold the same weights as often, so that one movmatrix makes all of it.
+//     It costs 200 requests 98.2 -> 100.0 us, four heads 45.8 -> 47.4, eight 34.0 -> 36.9.
 //   The weights' reference m follows the scores alone, w_t = 2^(x_t - m) up to 2^3, so
 //     the softmax sum knows nothing of V.  P stays within fp16 by a factor of its own,
 //     a power of two 2^k for each (head, group): P = w_t s_t,g 2^k.  It is lowered (with
@@ -42,7 +44,7 @@
 //     largest product is worked out only then.
 // What bounds it: the unpacking.  Per 16 tokens of a head (2304 bytes of K and V)
 // a warp issued about 310 instructions in fp16, 64 AND, 64 fp16 FMA and 16 matrix ones
-// among them (four or eight heads; with fewer, K's half of that is 16 AND, 16
+// among them (four or eight heads; with fewer, K's half of that is 16 AND, 8
 // shifts and 4 matrix ones).  One head a KV head, before and now: 200 requests, 458 MB,
 // 109 and 98 us; 8 x 32768 tokens x 32 heads 228 and 207 us (5.85 TB/s; copies alone run at 6.4).
 // Under sustained load the 1000 W cap takes the SM clock down by a tenth: 101 and 238 us.
@@ -146,6 +148,17 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// a - s * (the value that the pair a became in fp16, as the word h)
+__device__ __forceinline__ float2 sub_half2(float2 a, uint32_t h, float s) {
+  const float2 b = __half22float2(as_half2(h));
+  float2 d;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %6};\n\t"
+      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-s));
+  return d;
+}
+
 // d += a * b for one m16n8k32 tile, a of unsigned bytes, b of signed ones, 32-bit sums.
 __device__ __forceinline__ void mma16832_u8s8(int* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -156,21 +169,25 @@ __device__ __forceinline__ void mma16832_u8s8(int* d, const uint32_t* a, uint32_
 }
 constexpr uint32_t kNibbles = 0x0f0f0f0fu;
 
-// NH: query heads a lane keeps scores of: 2, or 1 where G is 1.  I8 (one or two
-// query heads): the scores by byte products, the queries' digits in the columns.
-template <typename T, int D, int NH, bool I8, bool MASS>
+// G: query heads per KV head.  NH: those a lane keeps scores of.  I8: the scores by
+// byte products, the queries' digits in the columns.
+template <typename T, int D, int G, bool MASS>
 __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, int heads_per_item) {
   using Cfg = Q4Config<T, D>;
   constexpr int TILE = Cfg::TILE, NSTAGE = Cfg::NSTAGE;
   constexpr int PIECES = D / 32, GROUPS = D / 64;
   constexpr int CB = kQ4ChunkBlocks;
+  constexpr bool I8 = G <= 2;
+  constexpr int NH = G == 1 ? 1 : 2;
+  // What the columns of P hold beside the heads: the groups (G <= 4), and what P's rounding left where room is left
+  constexpr bool GROUP_COLS = GROUPS == 2 && G <= 4, REST_COLS = G <= 2 || (G == 4 && GROUPS == 1);
   // m follows a score beyond 2^kMove: w s stays below 2^127.2, V's scales being below 2^124.2
   constexpr float kMove = 3.f;
   // P's factor 2^k is at most 2^126, lowered where P may pass kPMove, so that the largest lies in [2^10, 2^11):
   // by biased exponents, that of the largest w s and the factor's add up to kFactorPut
   constexpr float kPMove = 32768.f;
   constexpr int kFactorTop = 126 + 127, kFactorPut = 10 + 2 * 127;
-  constexpr int FG = I8 ? 1 : GROUPS;  // groups whose factor a lane keeps (I8: that of its own columns)
+  constexpr int FG = GROUP_COLS ? 1 : GROUPS;  // groups whose factor a lane keeps
 
   extern __shared__ __align__(128) uint8_t q4_smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + Cfg::WARPS * NSTAGE * Cfg::STAGE_BYTES);
@@ -179,7 +196,9 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, j = lane & 3;  // fragment row (query head, or dimension) and quad lane
-  const int G = a.q_per_kv, HK = a.heads, HQ = HK * G, PS = a.partition_size;
+  // the lane's heads are head0 and the next, its columns' group my_group (GROUP_COLS)
+  const int head0 = I8 ? 0 : G == 4 ? 2 * (j & 1) : 2 * j, my_group = G == 4 ? j >> 1 : j & 1;
+  const int HK = a.heads, HQ = HK * G, PS = a.partition_size;
   const int wph = Cfg::WARPS / heads_per_item;  // warps that share a KV head
   const int part = warp % wph;
 
@@ -238,7 +257,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
     const int chunks = (nblk + CB - 1) / CB;
     const int c_lo = chunks * part / wph, c_n = chunks * (part + 1) / wph - c_lo;
 
-    // of query heads 2 j + e (I8: heads e, the same in the quad's lanes); l_run is over this lane's tokens
+    // of query heads head0 + e; l_run is over this lane's tokens
     float m[NH], l_run[NH];
     float f[FG][NH];
 #pragma unroll
@@ -279,13 +298,12 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
       const uint32_t k0 = fills;
       for (int i = 0; i < NSTAGE && i < c_n; ++i) issue(k0 + i, c_lo + i);
 
-      // Q fragments, column r, dimensions 32 c + 8 j .. + 7: head r (I8: digit r / 2 of head r % 2); columns
-      // past G are zero
+      // Q fragments, column r, dimensions 32 c + 8 j .. + 7: head r % G (I8: digit r / 2 of head r % 2, zero past G)
       uint32_t qb[PIECES][I8 ? 2 : 4];
       float2 kq[NH];         // scores to log2 units, in two factors (I8: of this lane's digit)
       float qs[GROUPS][NH];  // I8: sum of a group's queries in this lane's digit
       {
-        const int q_head = I8 ? (r & 1) : r;
+        const int q_head = I8 ? (r & 1) : r & (G - 1);
         float qf[PIECES][8], top = 0.f;
 #pragma unroll
         for (int c = 0; c < PIECES; ++c) {
@@ -380,7 +398,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
           __syncwarp();
         }
 
-        // ---- scores of the chunk in log2 units: x[b][nt][e] of token 16 b + 8 nt + r, head 2 j + e (e)
+        // ---- scores of the chunk in log2 units: x[b][nt][e] of token 16 b + 8 nt + r, head head0 + e
         float x[CB][2][NH];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
@@ -476,13 +494,12 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         if constexpr (MASS) {
 #pragma unroll
           for (int e = 0; e < NH; ++e) {
-            if (!I8 && 2 * j + e >= G) continue;
-            float* dst = a.scores + (sh0 + (I8 ? e : 2 * j + e)) * a.score_stride + tok0 + (c_lo + i) * kQ4Chunk + r;
+            float* dst = a.scores + (sh0 + head0 + e) * a.score_stride + tok0 + (c_lo + i) * kQ4Chunk + r;
 #pragma unroll
             for (int b = 0; b < CB; ++b)
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt)  // I8: the quad's lanes hold the same, and store a block each
-                if ((!I8 || (b & 3) == j) && b * 16 + nt * 8 + r < valid)
+              for (int nt = 0; nt < 2; ++nt)  // lanes that hold the same heads store a block each in turn
+                if ((I8 ? (b & 3) == j : G == 8 || (b & 1) == j >> 1) && b * 16 + nt * 8 + r < valid)
                   dst[b * 16 + nt * 8] = x[b][nt][e];
           }
         }
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
                 const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(
-                    vt + b * TILE + q4_words_off(D) + (I8 ? (GROUPS == 2 ? j & 1 : 0) : gr) * 64 + nt * 32 + r * 4));
+                    vt + b * TILE + q4_words_off(D) + (GROUP_COLS ? my_group : gr) * 64 + nt * 32 + r * 4));
 #pragma unroll
                 for (int e = 0; e < NH; ++e) top[e] = fmaxf(top[e], x[b][nt][e] * sc);  // NaN does not count
               }
@@ -572,31 +589,37 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         for (int b = 0; b < CB; ++b) {
           const uint32_t tile = smem_addr(vt + b * TILE);
           const uint8_t* words = vt + b * TILE + q4_words_off(D);
-          uint32_t pc[2];  // I8: the quad's lanes take the groups' P in turn, each in columns of its own
-          if constexpr (I8) {
+          uint32_t pb[2], pr[2];  // P, and what its rounding left unless that has columns of its own
+          auto weights = [&](int gr) {
+            const int fg = FG == 1 ? 0 : gr;
+            float sc[2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const float sc = q4_scale(
-                  *reinterpret_cast<const uint32_t*>(words + (GROUPS == 2 ? (j & 1) * 64 : 0) + nt * 32 + r * 4));
-              const float2 p = mul2(mul2(make_float2(x[b][nt][0], x[b][nt][NH - 1]), make_float2(sc, sc)),
-                                    make_float2(f[0][0], f[0][NH - 1]));
-              pc[nt] = movmatrix(pack_half(p.x, NH == 2 ? p.y : 0.f));
+            for (int nt = 0; nt < 2; ++nt)
+              sc[nt] = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
+            // pairs of two heads, or of a head's two tokens
+#pragma unroll
+            for (int q = 0; q < NH; ++q) {
+              const float2 w = NH == 2 ? make_float2(x[b][q][0], x[b][q][NH - 1]) : make_float2(x[b][0][0], x[b][1][0]);
+              const float2 p = mul2(mul2(w, make_float2(sc[q], NH == 2 ? sc[q] : sc[1])), make_float2(f[fg][0], f[fg][NH - 1]));
+              const uint32_t hi = pack_half(p.x, p.y);
+              const float2 rest = sub_half2(p, hi, REST_COLS && j < 2 ? 0.f : 1.f);
+              if constexpr (NH == 1) {
+                pb[0] = movmatrix(pack_half(rest.x, 0.f));
+                pb[1] = movmatrix(pack_half(rest.y, 0.f));
+              } else {
+                const uint32_t part = pack_half(rest.x, rest.y);
+                pb[q] = movmatrix(REST_COLS ? part : hi);
+                if (!REST_COLS) pr[q] = movmatrix(part);
+              }
             }
-          }
+          };
+          if (FG == 1) weights(GROUP_COLS ? my_group : 0);
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
-            uint32_t pb[2];
+            if (FG == 2) weights(gr);
             __half2 nz[2];  // -z 2^-10 of tokens 2 j and 2 j + 1
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              if constexpr (I8) {
-                pb[nt] = pc[nt];
-              } else {
-                const float sc = q4_scale(*reinterpret_cast<const uint32_t*>(words + gr * 64 + nt * 32 + r * 4));
-                const float2 p = mul2(mul2(make_float2(x[b][nt][0], x[b][nt][NH - 1]), make_float2(sc, sc)),
-                                      make_float2(f[gr % FG][0], f[gr % FG][NH - 1]));
-                pb[nt] = movmatrix(pack_half(p.x, p.y));
-              }
               const uint2 two = *reinterpret_cast<const uint2*>(words + gr * 64 + nt * 32 + j * 8);
               nz[nt] = __hmul2(as_half2(__byte_perm(two.x, two.y, 0x5410)), as_half2(kMinus2m10));
             }
@@ -609,6 +632,10 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
               const uint32_t a1[4] = {q4_even(u0, nz[0]), q4_odd(u0, nz[0]), q4_even(u1, nz[1]), q4_odd(u1, nz[1])};
               mma16816<__half>(o[2 * gr + h][0], a0, pb[0], pb[1]);
               mma16816<__half>(o[2 * gr + h][1], a1, pb[0], pb[1]);
+              if constexpr (!REST_COLS) {
+                mma16816<__half>(o[2 * gr + h][0], a0, pr[0], pr[1]);
+                mma16816<__half>(o[2 * gr + h][1], a1, pr[0], pr[1]);
+              }
             }
           }
         }
@@ -699,56 +726,45 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         ml[e] = make_float2(m[e] + (float)up, l_run[e] * by);
       }
       // 2^-k
-      auto back = [&](int gr, int e) { return __uint_as_float((254u << 23) - __float_as_uint(f[gr % FG][e])); };
-      if constexpr (I8) {
-        // the lanes of a quad hold the same heads; with two groups, even lanes the first one's dimensions, odd
-        // ones the second's: each writes a piece
-        const int piece = GROUPS == 2 ? 2 * (j & 1) + (j >> 1) : j;
+      auto back = [&](int gr, int e) { return __uint_as_float((254u << 23) - __float_as_uint(f[FG == 1 ? 0 : gr][e])); };
+      // Of a head, this lane writes the pieces from `first` on, dimensions 32 c + 4 r .. + 3 of each.  With REST_COLS
+      // lanes 0 and 1 hold the sums of P, 2 and 3 those of what its rounding left: a lane gives the one that holds
+      // the other part its share of that one's piece.
+      constexpr int WRITES = REST_COLS ? 1 : GROUP_COLS ? 2 : PIECES;
+      const int first = REST_COLS ? (GROUP_COLS ? 2 * my_group : 0) + (j >> 1) : GROUP_COLS ? 2 * my_group : 0;
+      const bool writes = !(I8 && GROUPS == 1) || (j & 1) == 0;  // two lanes hold the same there
 #pragma unroll
-        for (int e = 0; e < NH; ++e) {
-          float v[4];
+      for (int e = 0; e < NH; ++e) {
 #pragma unroll
-          for (int c = 0; c < PIECES; ++c)
-            if (c == piece) {
+        for (int q = 0; q < WRITES; ++q) {
+          float v[4], give[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = o[c][k >> 1][2 * (k & 1) + e] * inv[e] * back(0, e);
-            }
-          if (piece < PIECES) {
-            if (!split)
-              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + e) * D + 32 * piece + 4 * r) =
-                  make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
-            else
-              *reinterpret_cast<float4*>(a.part_acc + ((sh0 + e) * a.max_parts + p) * D + 32 * piece + 4 * r) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-          }
-          if (lane == 0) {
-            if (split) a.part_ml[(sh0 + e) * a.max_parts + p] = ml[e];
-            else if (MASS) a.lse[sh0 + e] = m[e] + log2f(l_run[e]);
-          }
-        }
-      } else {
-        // this lane holds dimensions 32 c + 4 r .. + 3 of heads 2 j and 2 j + 1
+          for (int k = 0; k < 4; ++k) {
+            const int h = k >> 1, n = 2 * (k & 1) + e;
+            if constexpr (REST_COLS) {
 #pragma unroll
-        for (int e = 0; e < NH; ++e) {
-          const int h = 2 * j + e;
-          if (h >= G) continue;
-#pragma unroll
-          for (int c = 0; c < PIECES; ++c) {
-            const float lift = back(c / 2, e);
-            const float v[4] = {o[c][0][e] * inv[e] * lift, o[c][0][2 + e] * inv[e] * lift, o[c][1][e] * inv[e] * lift,
-                                o[c][1][2 + e] * inv[e] * lift};
-            if (!split) {
-              *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (sh0 + h) * D + 32 * c + 4 * r) =
-                  make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
+              for (int c = 0; c < PIECES; ++c) {
+                if (c == first) v[k] = o[c][h][n];
+                if (c == (first ^ 1)) give[k] = o[c][h][n];
+              }
+              v[k] += __shfl_xor_sync(kFullMask, give[k], 2);
             } else {
-              *reinterpret_cast<float4*>(a.part_acc + ((sh0 + h) * a.max_parts + p) * D + 32 * c + 4 * r) =
-                  make_float4(v[0], v[1], v[2], v[3]);
+              v[k] = GROUP_COLS && my_group ? o[(2 + q) % PIECES][h][n] : o[q][h][n];
             }
+            v[k] = v[k] * inv[e] * back(q / 2, e);
           }
-          if (r == 0) {
-            if (split) a.part_ml[(sh0 + h) * a.max_parts + p] = ml[e];
-            else if (MASS) a.lse[sh0 + h] = m[e] + log2f(l_run[e]);
-          }
+          if (!writes) continue;
+          const int64_t at = sh0 + head0 + e;
+          const int d = 32 * (first + q) + 4 * r;
+          if (!split)
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + d) =
+                make_uint2(MmaType<T>::pack(v[0], v[1]), MmaType<T>::pack(v[2], v[3]));
+          else
+            *reinterpret_cast<float4*>(a.part_acc + (at * a.max_parts + p) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (r == 0 && j < (G + 1) / 2) {
+          if (split) a.part_ml[(sh0 + head0 + e) * a.max_parts + p] = ml[e];
+          else if (MASS) a.lse[sh0 + head0 + e] = m[e] + log2f(l_run[e]);
         }
       }
     }
@@ -767,16 +783,14 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
         __threadfence();
         // rounds of at most 8 partitions of every head (each keeps its weights in registers)
         constexpr int RING = NSTAGE * Cfg::STAGE_BYTES, ROUND = 8 * D * 4;
-        constexpr auto buf = [](int g) { return g * ROUND < RING ? g * ROUND : RING; };
         bool merged = true;
-        if (G == 1) {
+        if constexpr (G == 1) {
           const int used = merge_staged<T, D, NSTAGE, RING, MASS>(a, sh0, np, lane, my_stages, my_bars, fills);
           fills += used > 0 ? used : -used;
           merged = used > 0;
         } else {
-          merged = G == 8   ? merge_group<T, D, 8, NSTAGE, buf(8), MASS>(a, sh0, np, lane, my_stages, my_bars, fills)
-                   : G == 4 ? merge_group<T, D, 4, NSTAGE, buf(4), MASS>(a, sh0, np, lane, my_stages, my_bars, fills)
-                            : merge_group<T, D, 2, NSTAGE, buf(2), MASS>(a, sh0, np, lane, my_stages, my_bars, fills);
+          merged = merge_group<T, D, G, NSTAGE, G * ROUND < RING ? G * ROUND : RING, MASS>(a, sh0, np, lane, my_stages,
+                                                                                          my_bars, fills);
         }
         if (!merged && lane == 0) {  // as for a copy of the item: report, stop, poison the plan
           atomicOr(a.err, PA_DEVERR_TIMEOUT);

@@ -323,9 +323,10 @@ template <typename T, int D>
 cudaError_t set_q4_attrs() {
   const int smem = (int)Q4Config<T, D>::smem_bytes(kMaxPartition);
   cudaError_t e = cudaSuccess;
-  for (auto kernel : {paged_decode_q4_kernel<T, D, 1, true, false>, paged_decode_q4_kernel<T, D, 1, true, true>,
-                      paged_decode_q4_kernel<T, D, 2, true, false>, paged_decode_q4_kernel<T, D, 2, true, true>,
-                      paged_decode_q4_kernel<T, D, 2, false, false>, paged_decode_q4_kernel<T, D, 2, false, true>})
+  for (auto kernel : {paged_decode_q4_kernel<T, D, 1, false>, paged_decode_q4_kernel<T, D, 1, true>,
+                      paged_decode_q4_kernel<T, D, 2, false>, paged_decode_q4_kernel<T, D, 2, true>,
+                      paged_decode_q4_kernel<T, D, 4, false>, paged_decode_q4_kernel<T, D, 4, true>,
+                      paged_decode_q4_kernel<T, D, 8, false>, paged_decode_q4_kernel<T, D, 8, true>})
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
@@ -540,12 +541,13 @@ cudaError_t launch_decode(const DecodeArgs& a, const DeviceState& dev, cudaStrea
 template <typename T, int D>
 cudaError_t launch_q4(const DecodeArgs& a, const DeviceState& dev, cudaStream_t stream, bool overlap) {
   using Cfg = Q4Config<T, D>;
-  auto kernel = a.q_per_kv == 1   ? (a.scores ? paged_decode_q4_kernel<T, D, 1, true, true>
-                                             : paged_decode_q4_kernel<T, D, 1, true, false>)
-                : a.q_per_kv == 2 ? (a.scores ? paged_decode_q4_kernel<T, D, 2, true, true>
-                                              : paged_decode_q4_kernel<T, D, 2, true, false>)
-                                  : (a.scores ? paged_decode_q4_kernel<T, D, 2, false, true>
-                                              : paged_decode_q4_kernel<T, D, 2, false, false>);
+  auto kernel = a.scores ? paged_decode_q4_kernel<T, D, 1, true> : paged_decode_q4_kernel<T, D, 1, false>;
+  if (a.q_per_kv == 2)
+    kernel = a.scores ? paged_decode_q4_kernel<T, D, 2, true> : paged_decode_q4_kernel<T, D, 2, false>;
+  else if (a.q_per_kv == 4)
+    kernel = a.scores ? paged_decode_q4_kernel<T, D, 4, true> : paged_decode_q4_kernel<T, D, 4, false>;
+  else if (a.q_per_kv == 8)
+    kernel = a.scores ? paged_decode_q4_kernel<T, D, 8, true> : paged_decode_q4_kernel<T, D, 8, false>;
   const int64_t upper = (int64_t)a.num_seqs * a.max_parts * a.head_groups;
   const int grid = (int)std::min<int64_t>(upper, (int64_t)dev.num_sms * Cfg::CTAS_PER_SM);
   return launch_decode_grid(kernel, grid, Cfg::THREADS, Cfg::smem_bytes(a.partition_size), stream, a,

@@ -7,7 +7,7 @@ scale, n - z a held value; every bound is for one dimension of one head):
   * the output's own rounding, eps / 2 of it (and half a subnormal step);
   * scores: fp32 sums, off by at most D 2^-24 scale sum |q| s (n + |z|) + 2^-22 =: e, numerator
     and denominator: 2 e sum w |v|;
-  * P = w s 2^k rounded to fp16: 2^-11 of it, and where it is subnormal 2^-25.  2^k puts the
+  * P = w s 2^k held as two fp16 numbers: 2^-21 of it, and where they are subnormal 2^-25.  2^k puts the
     largest w s so far at 2^10 or above (2^3 at least where k meets its limit of 126: scales down
     to 2^-123): a subnormal is off by 2^-28 of the largest, times |n - z|;
   * the sum of the numerator: L 2^-23 sum w |v|;
@@ -25,7 +25,7 @@ from tests.test_gpu_q4 import TYPES, as_type, check, cuda, decode_case, run_deco
 
 pytestmark = pytest.mark.gpu
 
-ROUNDED = 2.0 ** -11  # of a weight times its scale
+ROUNDED = 2.0 ** -21  # of a weight times its scale
 
 
 @pytest.fixture(autouse=True)
@@ -175,3 +175,11 @@ def test_keys_at_the_ends_of_the_range(k_size, heads, group, dim):
     c = decode_case(group * dim, [200, 17], heads, group, dim, "bf16", sized(np.full(217, k_size), np.full(217, 1.0)))
     c["q"], c["qx"] = as_type(c["qx"] / k_size, "bf16")
     check_decode_and_mass(c, (0, 64))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group", [(1, 1), (6, 1), (3, 2), (1, 4), (4, 4), (2, 8)])
+def test_weights_keep_their_precision(heads, group, dim):
+    """fp16 values whose sum nearly cancels: what the weights' rounding leaves shows. Small scores keep e below it."""
+    lengths = [2, 5, 16, 33, 64, 100]
+    check_decode_and_mass(decode_case(heads + dim, lengths, heads, group, dim, "f16", sized(np.full(220, 0.05), np.full(220, 1.0))), (0, 16))
