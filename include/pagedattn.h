@@ -460,7 +460,10 @@ typedef struct pa_track {
  * buffers, else they must not overlap; with `out` apart, a repeated call
  * repeats the same moves.
  * keep_lens: device int32 [num_seqs]; a negative one sets
- * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole.  The blocks of every
+ * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole.  A token that stays but
+ * whose old or new slot is in a block outside the pool is lost: the call sets
+ * PA_DEVERR_BLOCK_ID, and the slot that it was to take keeps its own token, with
+ * that one's mass and position in the track.  The blocks of every
  * evicted sequence must be private to it (copy them on write first).  All
  * pool types.  At most 65535 sequences and contexts of 2^30 tokens.
  * workspace: pa_evict_workspace_bytes().

@@ -301,19 +301,26 @@ __global__ void __launch_bounds__(256)
   for (int m0 = blockIdx.x * kEvictMovesPerCta; m0 < head.x; m0 += gridDim.x * kEvictMovesPerCta) {
     const int n = min(kEvictMovesPerCta, head.x - m0);
     __syncthreads();  // slots are free again
-    if (threadIdx.x < 2 * n) {
-      const int2 mv = a.moves[(int64_t)s * a.move_cap + m0 + threadIdx.x / 2];
+    if (threadIdx.x < 32) {  // two lanes a move: its source and its destination
+      const bool live = threadIdx.x < 2 * n;
+      const int2 mv = live ? a.moves[(int64_t)s * a.move_cap + m0 + threadIdx.x / 2] : make_int2(0, 0);
       const int t = (threadIdx.x & 1) ? mv.y : mv.x;
-      int32_t b = table[t / kBlock];
-      if (b < 0 || b >= a.num_blocks) {
-        atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-        b = -1;
+      int slot = -1;
+      if (live) {
+        const int32_t b = table[t / kBlock];
+        if (b < 0 || b >= a.num_blocks) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+        else slot = b * kBlock + t % kBlock;
       }
-      reinterpret_cast<int*>(slots)[threadIdx.x] = b < 0 ? -1 : b * kBlock + t % kBlock;
-      if ((threadIdx.x & 1) == 0) {  // the token's track; its old slot starts from 0 again
-        const int64_t in = s * a.in_stride + mv.x, out = s * a.out_stride;
+      const int other = __shfl_xor_sync(kFullMask, slot, 1);  // by all lanes, before any condition
+      const bool whole = slot >= 0 && other >= 0;
+      if (live) reinterpret_cast<int*>(slots)[threadIdx.x] = whole ? slot : -1;
+      if (live && (threadIdx.x & 1) == 0) {
+        // the token's track; its old slot starts from 0 again.  A move from or to a bad block is dropped: the
+        // destination keeps its own token, and that one's track
+        const int from = whole ? mv.x : mv.y;
+        const int64_t in = s * a.in_stride + from, out = s * a.out_stride;
         const float mass = a.mass_in[in];
-        const int at = mv.x < head.y ? a.positions_in[in] : head.z + mv.x - head.y;
+        const int at = from < head.y ? a.positions_in[in] : head.z + from - head.y;
         a.mass_out[out + mv.y] = mass;
         a.positions_out[out + mv.y] = at;
         a.mass_out[out + mv.x] = 0.f;
