@@ -91,7 +91,8 @@ typedef enum {
 /* Bits of the device error word (pa_device_errors). */
 #define PA_DEVERR_BLOCK_ID 0x1u    /* block table entry outside [0, num_blocks) */
 #define PA_DEVERR_SLOT 0x2u        /* slot outside [0, num_blocks * block_size) */
-#define PA_DEVERR_CONTEXT_LEN 0x4u /* context_len < 0 or above the table / max bound */
+#define PA_DEVERR_CONTEXT_LEN 0x4u /* context_len < 0 or above the table / max bound; eviction:
+                                      a negative budget, or a history that does not fit */
 #define PA_DEVERR_PAIR 0x8u        /* copy_blocks pair outside the pool */
 #define PA_DEVERR_TIMEOUT 0x10u    /* an mbarrier wait ran past its limit */
 #define PA_DEVERR_PLAN 0x20u       /* the workspace holds no plan this launch may run, or a
@@ -460,7 +461,10 @@ typedef struct pa_track {
  * buffers, else they must not overlap; with `out` apart, a repeated call
  * repeats the same moves.
  * keep_lens: device int32 [num_seqs]; a negative one sets
- * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole.  A token that stays but
+ * PA_DEVERR_CONTEXT_LEN and keeps its sequence whole; so does, where the sequence is
+ * over its budget, a history that does not fit it: held or next negative, held above
+ * context_lens[s] (a sequence must not shrink below held by other means), or positions
+ * that would pass 2^31 - 1.  A token that stays but
  * whose old or new slot is in a block outside the pool is lost: the call sets
  * PA_DEVERR_BLOCK_ID, and the slot that it was to take keeps its own token, with
  * that one's mass and position in the track.  The blocks of every

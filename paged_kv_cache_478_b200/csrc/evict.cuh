@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_select_kernel(EvictArg
   float* mass_out = a.mass_out + s * a.out_stride;
   int32_t* pos_out = a.positions_out + s * a.out_stride;
   const int held = a.history_in[2 * s], next = a.history_in[2 * s + 1];
+  // a history that is not this sequence's (it shrank below `held`, or positions pass 32 bits): nothing is evicted
+  if (keep < L && ((uint32_t)held > (uint32_t)L || (uint32_t)next > (uint32_t)(INT32_MAX - (L - held)))) {
+    if (rank == 0 && tid == 0) atomicOr(a.err, PA_DEVERR_CONTEXT_LEN);
+    keep = L;
+  }
   // this CTA's slots, each warp's of them contiguous and a multiple of 32
   const int per = (L + C * kEvictThreads - 1) / (C * kEvictThreads) * kEvictThreads;
   const int lo = min(L, rank * per), hi = min(L, lo + per);
