@@ -33,7 +33,7 @@
 //     (up to four heads), times the two parts where room is left (one or two heads,
 //     or four at head_dim 64); else the second part takes products of its own.  The
 //     quad's lanes hold the same weights as often, so that one movmatrix makes all of it.
-//     It costs 200 requests 98.2 -> 100.0 us, four heads 45.8 -> 47.4, eight 34.0 -> 36.9.
+//     It costs 200 requests 98.3 -> 100.3 us, four heads 45.7 -> 47.5, eight 34.4 -> 36.9.
 //   The weights' reference m follows the scores alone, w_t = 2^(x_t - m) up to 2^3, so
 //     the softmax sum knows nothing of V.  P stays within fp16 by a factor of its own,
 //     a power of two 2^k for each (head, group): P = w_t s_t,g 2^k.  It is lowered (with
@@ -42,15 +42,16 @@
 //     to 2^-24 of the largest w_t s_t,g so far, whatever the scales of V.  Whether one
 //     could pass 2^15 is told from the chunk's largest weight and largest scale; the
 //     largest product is worked out only then.
-// What bounds it: the unpacking.  Per 16 tokens of a head (2304 bytes of K and V)
-// a warp issued about 310 instructions in fp16, 64 AND, 64 fp16 FMA and 16 matrix ones
-// among them (four or eight heads; with fewer, K's half of that is 16 AND, 8
-// shifts and 4 matrix ones).  One head a KV head, before and now: 200 requests, 458 MB,
-// 109 and 98 us; 8 x 32768 tokens x 32 heads 228 and 207 us (5.85 TB/s; copies alone run at 6.4).
-// Under sustained load the 1000 W cap takes the SM clock down by a tenth: 101 and 238 us.
-// 64 requests x 8 KV heads x 8 query heads, 77 MB: 34 us (plan entry, table and first
-// copies 5 us, six chunks 16, merge 5).
-// Tried on the fp16 form and slower (the long case): 16 warps an SM at 128 registers
+// What bounds it: the unpacking.  Per 16 tokens of a KV head (2304 bytes of K and V) a
+// launch issues 280 warp instructions in all with one query head, 375 with four and 403
+// with eight; the unpacking itself is 64 AND and 64 fp16 FMA (with one or two heads K's
+// half of that is 16 AND and 8 shifts).  Measured: one head, 200 requests, 515 MB, 100
+// us; 8 x 32768 tokens x 32 heads 209 us (5.8 TB/s; copies alone run at 6.4; K by fp16
+// too took about a tenth more).  Under sustained load the 1000 W cap takes the SM clock
+// down by a tenth: 104 and 243 us.  Two heads, 200 x 16 KV heads, 258 MB: 68 us; four, 200
+// x 8, 129 MB: 47 us; eight, 64 x 8, 77 MB: 37 us, one wave of items (plan entry, table and
+// first copies 5 us, about six chunks of 3, merge 5).
+// Tried on the fp16 form, when it took 227 us, and slower (the long case): 16 warps an SM at 128 registers
 // (241 us), copying warps of their own with four heads a copy (242; with setmaxnreg
 // 275), warps that take single heads by themselves (257), K as 64 + n with the constant
 // taken off the sums (242), the shifts on the multiply pipe (256), e4m3 operands (285;
@@ -151,12 +152,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // a - s * (the value that the pair a became in fp16, as the word h)
 __device__ __forceinline__ float2 sub_half2(float2 a, uint32_t h, float s) {
   const float2 b = __half22float2(as_half2(h));
-  float2 d;
-  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %6};\n\t"
-      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-s));
-  return d;
+  return make_float2(fmaf(-s, b.x, a.x), fmaf(-s, b.y, a.y));
 }
 
 // d += a * b for one m16n8k32 tile, a of unsigned bytes, b of signed ones, 32-bit sums.
