@@ -6,8 +6,10 @@
 // they also store it (4 bytes a token and query head, against 4 D bytes of
 // 16-bit K and V) and, per query head, the logarithm of its softmax sum, which
 // is known only when the sequence's last partition is merged.  This kernel
-// then turns the scores into weights and adds the heads in a fixed order, so
-// that the result does not depend on how the work was split.
+// then turns the scores into weights and adds the heads in a fixed order: for
+// the same sizes and partition the result is the same from run to run.  (The
+// logarithms are rounded as the work was split, into partitions and, in 4-bit
+// pools, over a head's warps, so another partition may change the last bits.)
 #pragma once
 
 #include <math.h>

@@ -126,13 +126,14 @@ cudaError_t set_decode_attrs_all_groups() {
 // KV heads one work item covers, for G query heads per KV head.
 int rings_for(int G) { return warps_for(G) / G; }
 
+// 4-bit pools have kernels of their own (decode_q4.cuh), whatever the grouping.
+bool is_q4(const pa_pool* pool) { return pool->dtype == PA_Q4_F16 || pool->dtype == PA_Q4_BF16; }
+
 // Groups of 2, 4 or 8 query heads on fp16/bf16 pools take the tensor-core
 // kernel (two warps per KV head); MHA and fp32 pools take the CUDA-core
 // kernel.  (Pairs once ran faster on CUDA cores; since the tensor-core
 // kernel stages whole tiles and merges all heads of a KV head at once it
 // is faster for them too: 106 -> 89 us on 200 requests x 8 KV heads.)
-bool is_q4(const pa_pool* pool) { return pool->dtype == PA_Q4_F16 || pool->dtype == PA_Q4_BF16; }
-
 bool use_gqa_mma(const pa_pool* pool) {
   return pool->q_per_kv >= 2 && (pool->dtype == PA_F16 || pool->dtype == PA_BF16);
 }
@@ -499,12 +500,15 @@ int auto_partition(int num_seqs, int head_groups, int max_context_len, int slots
 // results and merge: about 6 us) weighs four times as much as on 16-bit pools,
 // so partitions are long where the batch allows it: about 3.6 times as many
 // tokens of the longest sequences as the slots, at most 2048 a partition
-// (200 requests x 32 heads up to 2048: 98 us at 2048, 103 at 1024, 112 at 512;
-// 200 x 8 KV heads: 46 us at 512, 54 at 256 and at 768, 86 at 1536, where the
-// longest items outlast the rest; 8 x 32768 x 32 heads: 207 at 2048, 229 at 512).
+// (200 requests x 32 heads up to 2048: 102 us at 2048, 107 at 1024, 115 at 512;
+// 200 x 8 KV heads: 49 us at 512, 57 at 256 and at 768, 95 at 1536, where the
+// longest items outlast the rest; 8 x 32768 x 32 heads: 210 at 2048, 242 at 512).
 // A small batch gets one item per slot, the mean length taken as half the
 // longest, as long as that keeps partitions within 512 (64 x 8 KV heads up to
-// 2048: 34 us at 384, one item per slot; 41 at 256, 39 at 512).  Whole chunks.
+// 2048, 8 query heads: 37 us at 384, one item per slot; 43 at 256 and at 512).
+// Whole chunks.  At head_dim 64 the same shapes have their best where the rule puts
+// them; for a single sequence of 32768 tokens it misses (8 KV heads: 57 us at its 256,
+// 44 at 512).
 int auto_partition_q4(int num_seqs, int head_groups, int max_context_len, int slots) {
   const int64_t tokens = (int64_t)num_seqs * head_groups * std::max(16, max_context_len);
   // sequences of mean length m give about m / ps + 1 / 2 partitions each

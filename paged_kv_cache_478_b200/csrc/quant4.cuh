@@ -21,8 +21,9 @@
 // those of exact quotients (q4_quotient).  Measured (32 heads x 128 fp16):
 // append of 16384 tokens 86 us, 1024 blocks to 4 bits 69 us and back 65 us, for
 // 344 MB each (4.0, 5.0 and 5.3 TB/s): bound by instructions one way, and by the
-// latency of its loads the other (n - z two at a time, in fp16: no faster).  A group that holds an infinity or NaN, or whose
-// range passes fp32, gets s = NaN and reads back as NaN.
+// latency of its loads the other, where n - z two at a time in fp16 was no faster.
+// A group that holds an infinity or NaN, or whose range passes fp32, gets s = NaN
+// and reads back as NaN.
 #pragma once
 
 #include <math.h>
