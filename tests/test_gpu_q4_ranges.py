@@ -183,3 +183,48 @@ def test_weights_keep_their_precision(heads, group, dim):
     """fp16 values whose sum nearly cancels: what the weights' rounding leaves shows. Small scores keep e below it."""
     lengths = [2, 5, 16, 33, 64, 100]
     check_decode_and_mass(decode_case(heads + dim, lengths, heads, group, dim, "f16", sized(np.full(220, 0.05), np.full(220, 1.0))), (0, 16))
+
+
+# ---- signs, zeros and NaN in every head layout -----------------------------------------------------
+
+LAYOUTS = [(1, 1, 64), (5, 1, 128), (2, 2, 64), (3, 2, 128), (2, 4, 64), (1, 4, 128), (1, 8, 64), (4, 8, 128)]
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
+@pytest.mark.parametrize("heads,group,dim", LAYOUTS)
+def test_scales_of_any_sign(scale, heads, group, dim):
+    c = decode_case(dim + group, [100, 17, 64, 1], heads, group, dim, "f16", sized(np.full(182, 0.1), np.full(182, 1.0)))
+    check_decode_and_mass(dict(c, scale=scale), (0, 32))
+
+
+@pytest.mark.parametrize("heads,group,dim", LAYOUTS)
+@pytest.mark.parametrize("partition", [0, 16, 64])
+def test_queries_that_are_zero_or_not_finite_stay_with_their_head(heads, group, dim, partition):
+    c = decode_case(3 * dim + group, [150, 33], heads, group, dim, "bf16")
+    plain = run_decode(c, partition)
+    for value, at in ((0.0, 0), (float("nan"), heads * group - 1), (float("inf"), heads * group // 2), (float("-inf"), 0)):
+        q = c["q"].clone()
+        q[0, at, 5 if value else slice(None)] = value
+        got = run_decode(dict(c, q=q), partition)
+        others = [h for h in range(heads * group) if h != at]
+        assert torch.equal(got[0, others], plain[0, others]) and torch.equal(got[1], plain[1])
+        if value == 0.0:  # the mean of the values
+            v = oc.values(c["vp"], dim)[c["tables"][0, np.arange(150) // 16], 0, np.arange(150) % 16]
+            # the output's rounding, and 150 2^-23 of the sum (weights are exactly 1)
+            assert (np.abs(got[0, at].double().cpu().numpy() - v.mean(0)) <= 2.0 ** -8 * np.abs(v.mean(0)) + 2.0 ** -14 * np.abs(v).mean(0)).all()
+        else:
+            assert torch.isnan(got[0, at]).all()
+
+
+@pytest.mark.parametrize("heads,group", [(2, 1), (3, 2), (1, 4), (2, 8)])
+@pytest.mark.parametrize("partition", [0, 16])
+def test_values_that_are_not_finite_stay_with_their_group(heads, group, partition):
+    c = decode_case(90 + group, [70, 20], heads, group, 128, "f16")
+    plain = run_decode(c, partition)
+    row = oc.values(c["vp"], 128)[c["tables"][0, 2], heads - 1, 7].copy()
+    row[70] = np.inf
+    oc.store_row(c["vp"], c["tables"][0, 2], heads - 1, 7, row)
+    got = run_decode(c, partition)
+    hit = slice((heads - 1) * group, None)
+    assert torch.isnan(got[0, hit, 64:]).all() and torch.equal(got[0, hit, :64], plain[0, hit, :64])
+    assert torch.equal(got[0, :(heads - 1) * group], plain[0, :(heads - 1) * group]) and torch.equal(got[1], plain[1])
