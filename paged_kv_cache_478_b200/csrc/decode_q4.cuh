@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(128, 3) paged_decode_q4_kernel(DecodeArgs a, i
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFullMask, mx[e], k));
           down[e] = 0.f;
-          if (mx[e] > m[e] + kMove) {
+          if (mx[e] - m[e] > kMove) {  // by the difference: beyond 2^24 the sum would be rounded
             down[e] = m[e] - mx[e];  // -infinity on the first move
             m[e] = mx[e];
             l_run[e] *= ex2(down[e]);

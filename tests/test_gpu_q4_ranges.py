@@ -228,3 +228,25 @@ def test_values_that_are_not_finite_stay_with_their_group(heads, group, partitio
     hit = slice((heads - 1) * group, None)
     assert torch.isnan(got[0, hit, 64:]).all() and torch.equal(got[0, hit, :64], plain[0, hit, :64])
     assert torch.equal(got[0, :(heads - 1) * group], plain[0, :(heads - 1) * group]) and torch.equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("heads,group,dim", LAYOUTS)
+def test_scores_beyond_whole_numbers_steps(heads, group, dim):
+    """Scores of 2^25 and more, whose neighbours in fp32 lie 4 apart, with values near the type's largest: one token
+    takes all the weight, whichever it is, and the output is its value."""
+    c = decode_case(group + dim, [90], heads, group, dim, "bf16", sized(np.full(90, 1.0), np.full(90, 2e37)))
+    base = np.sign(np.random.default_rng(5).standard_normal(dim))
+    c["q"], c["qx"] = as_type(np.tile(base, (1, heads * group, 1)), "bf16")
+    order = np.random.default_rng(6).permutation(90)  # rising and falling, far apart: 2^18 and more between any two
+    for t in range(90):
+        for h in range(heads):
+            oc.store_row(c["kp"], c["tables"][0, t // 16], h, t % 16, as_type((2.0 ** 18 + 2.0 ** 13 * order[t]) * base, "bf16")[1])
+    c["scale"] = 16.0
+    k = oc.values(c["kp"], dim)[c["tables"][0, np.arange(90) // 16], :, np.arange(90) % 16]
+    x = np.einsum("thd,d->ht", k, base)
+    first = x.argmax(1)
+    assert ((x == x.max(1, keepdims=True)).sum(1) == 1).all()
+    v = oc.values(c["vp"], dim)[c["tables"][0, first // 16], np.arange(heads), first % 16]
+    want = torch.from_numpy(v).to(torch.bfloat16).repeat_interleave(group, 0)
+    for partition in (0, 16, 64):
+        assert torch.equal(run_decode(c, partition)[0].cpu(), want)
